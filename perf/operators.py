@@ -1,5 +1,6 @@
-"""Measured cases of the cache operators: rotary positions (alone and fused with the append to the KV
-cache), the attention weight each cached key receives, and eviction of the lightest keys.
+"""Measured cases of the operators around the KV cache: rotary positions (alone and fused with the append),
+attention with capped or biased scores and per-row key ranges (documents, prefixes) with its gradients and its form
+for one token, the attention weight each cached key receives, and eviction of the lightest keys.
 
 Every case runs in two forms. With ``own`` false, ``run`` computes it from elementary torch operations in 32 bits
 (angles in 64); with ``own`` true it makes the calls a user of the library makes. ``exact`` computes the same
@@ -44,6 +45,13 @@ def _evict(name=None, *, B, h_kv, T, budget, d, shortest=0, sink=0, recent=0, pa
     return dict(c, name=name) if name else c
 
 
+def _attend(name=None, *, B, h_q, h_kv, S, T, d, cap=0.0, alibi=False, docs=0, prefix=0, causal=True, window=0,
+            grad=False, page=0, shortest=0, dtype="bf16"):
+    c = dict(op="attend", B=B, h_q=h_q, h_kv=h_kv, S=S, T=T, d=d, cap=cap, alibi=alibi, docs=docs, prefix=prefix,
+             causal=causal, window=window, grad=grad, page=page, shortest=shortest or T, dtype=dtype)
+    return dict(c, name=name) if name else c
+
+
 def listed():
     return [
         # one new token of eight sequences: its q and k rotated, k and v appended (every decode step)
@@ -51,28 +59,28 @@ def listed():
         # a 512-token prompt chunk of four sequences into 16-token pages, interleaved pairs, stretched context
         _append("append_chunk_paged", B=4, h_q=32, h_kv=8, S=512, T=2048, d=128, rot=128, interleaved=True, page=16,
                 yarn=8.0),
-        # the queries of long prompts, read in place from a fused q/k/v projection (B, S, 48 heads, 128)
-        _rope("rope_long_prompt", B=2, h=32, S=8192, d=128, rot=128, fused=16),
-        # the gradient of a partial rotation in fp32 with odd sizes, at far positions
-        _rope("rope_gradient_fp32", B=3, h=5, S=1023, d=80, rot=20, offset=12, inverse=True, start=100000,
-              dtype="fp32"),
+        # the gradient of the rotation for long prompts, read in place from a fused q/k/v buffer (B, S, 48 heads, 128)
+        _rope("rope_gradient_long", B=2, h=32, S=8192, d=128, rot=128, fused=16, inverse=True),
+        # a 4096-token prompt whose scores are capped, causal
+        _attend("prefill_capped", B=1, h_q=32, h_kv=8, S=4096, T=4096, d=128, cap=50.0),
+        # a training step over twelve documents packed into one 4096-token row, distance bias: outputs and gradients
+        _attend("train_documents_biased", B=1, h_q=32, h_kv=8, S=4096, T=4096, d=128, alibi=True, docs=12, grad=True),
+        # one token of eight ragged sequences over 16-token pages, capped and biased
+        _attend("decode_capped_biased", B=8, h_q=32, h_kv=8, S=1, T=8192, d=128, cap=30.0, alibi=True, page=16,
+                shortest=2001),
+        # check mode: a small fp32 training step with a bidirectional prefix, capped, odd sizes
+        _attend("train_prefix_fp32", B=2, h_q=6, h_kv=2, S=67, T=67, d=96, cap=20.0, prefix=13, causal=False,
+                grad=True, dtype="fp32"),
         # the weight one decoded token gives every cached key, added to the running totals
         _weights("weights_one_token", B=8, h_q=32, h_kv=8, S=1, T=8192, d=128, accumulate=True),
-        # the same over ragged sequences in 16-token pages, NaN behind each sequence
-        _weights("weights_one_token_paged", B=16, h_q=32, h_kv=8, S=1, T=8192, d=128, shortest=1021, page=16),
-        # the last 33 queries of a prompt score a long history before it is cut
-        _weights("weights_last_queries", B=2, h_q=32, h_kv=8, S=33, T=32768, d=128, shortest=30001),
+        # the last 33 queries of prompts score long ragged histories in 16-token pages, NaN behind each sequence
+        _weights("weights_last_queries", B=2, h_q=32, h_kv=8, S=33, T=32768, d=128, shortest=21001, page=16),
         # every query of a 4096-token prompt, causal
         _weights("weights_whole_prompt", B=1, h_q=32, h_kv=8, S=4096, T=4096, d=128),
-        # check mode: fp32, odd head width, odd lengths, a sliding window
-        _weights("weights_fp32_window", B=2, h_q=6, h_kv=2, S=17, T=515, d=96, shortest=300, window=100,
-                 dtype="fp32"),
         # eight sequences of 8192 keys cut to a quarter, into a smaller cache
         _evict("evict_to_quarter", B=8, h_kv=8, T=8192, budget=2048, d=128, sink=4, recent=256),
         # long ragged histories in 16-token pages, into fresh pages of the same pool
         _evict("evict_long_paged", B=4, h_kv=8, T=32768, budget=4096, d=128, shortest=3001, sink=4, recent=512, page=16),
-        # a small fp32 cache of odd sizes
-        _evict("evict_small_fp32", B=2, h_kv=3, T=333, budget=101, d=80, shortest=57, sink=1, recent=16, dtype="fp32"),
     ]
 
 
@@ -81,9 +89,9 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["append", "rope", "weights", "weights", "evict", "evict"])
+    op = rng.choice(["append", "rope", "attend", "attend", "decode", "weights", "weights", "evict"])
     dtype = rng.choice(["bf16", "bf16", "bf16", "fp32"])
-    d = rng.choice([64, 128]) if dtype == "bf16" and op == "weights" else rng.choice([64, 72, 80, 96, 128, 128, 192, 256])
+    d = rng.choice([64, 128]) if dtype == "bf16" and op in ("weights", "attend", "decode") else rng.choice([64, 72, 80, 96, 128, 128, 192, 256])
     h_kv = rng.choice([1, 2, 3, 4, 8])
     r = rng.choice([1, 2, 3, 4, 7, 8, 16]) if h_kv < 8 else rng.choice([1, 2, 4])
     page = rng.choice([0, 0, 16, 64, 48])
@@ -116,6 +124,23 @@ def draw(rng):
         return _weights(B=B, h_q=h_kv * r, h_kv=h_kv, S=S, T=T, d=d, shortest=rng.randint(S, T),
                         window=rng.choice([0, 0, 0, _log(rng, 1, T)]), page=page, accumulate=rng.random() < 0.5,
                         dtype=dtype)
+    if op in ("attend", "decode"):
+        cap, alibi = rng.choice([(0.0, True), (0.0, False), (20.0, False), (50.0, False), (30.0, True)])
+        if op == "decode":
+            T = up(_log(rng, 1, 32768 if dtype == "bf16" else 4096))
+            B = max(1, min(rng.randint(1, 16), 60000000 // (h_kv * T * d)))
+            return _attend(B=B, h_q=h_kv * r, h_kv=h_kv, S=1, T=T, d=d, cap=cap, alibi=alibi,
+                           window=rng.choice([0, 0, _log(rng, 1, T)]), page=page, shortest=rng.randint(1, T), dtype=dtype)
+        T = _log(rng, 2, 4096 if dtype == "bf16" else 512)
+        S = T if rng.random() < 0.7 else rng.randint(2, T)
+        mask = rng.choice(["none", "docs", "prefix", "window"]) if S == T else "none"
+        room = (500000000 if dtype == "bf16" else 10000000) // (h_kv * r * S * T)
+        h_kv = h_kv if room else 1
+        B = max(1, min(rng.randint(1, 8), room))
+        return _attend(B=B, h_q=h_kv * r, h_kv=h_kv, S=S, T=T, d=d, cap=cap, alibi=alibi,
+                       docs=rng.randint(1, min(T, 16)) if mask == "docs" else 0,
+                       prefix=rng.randint(1, T) if mask == "prefix" else 0, causal=mask != "prefix",
+                       window=_log(rng, 1, T) if mask == "window" else 0, grad=rng.random() < 0.5, dtype=dtype)
     T = up(_log(rng, 2, 32768))
     budget = _log(rng, 1, T)
     sink = rng.choice([0, 0, min(4, budget)])
@@ -130,6 +155,22 @@ def _lengths(c):
     return [c["T"] - (c["T"] - c["shortest"]) * b // max(1, c["B"] - 1) for b in range(c["B"])]
 
 
+def _documents(c):
+    """First and last-but-one positions of the documents packed into a row: shorter ones first."""
+    if not c["docs"]:
+        return [(0, c["T"])]
+    cut = [int(c["T"] * (i / c["docs"]) ** 1.4) for i in range(c["docs"] + 1)]
+    return [(lo, hi) for lo, hi in zip(cut, cut[1:]) if hi > lo]
+
+
+def _ranges(c):
+    """(S, 2): the keys lo <= j < hi that each row's document and prefix let it see (S = T rows)."""
+    out = []
+    for lo, hi in _documents(c):
+        out += [(lo, min(hi, max(p + 1, lo + c["prefix"]))) for p in range(lo, hi)]
+    return out
+
+
 def work(c):
     e = 2 if c["dtype"] == "bf16" else 4
     if c["op"] == "rope":
@@ -139,6 +180,21 @@ def work(c):
         rows = c["B"] * c["S"] * (c["h_q"] + 2 * c["h_kv"])
         return {"bytes": 2 * e * rows * c["d"], "flops": 3 * c["B"] * c["S"] * (c["h_q"] + c["h_kv"]) * c["rot"]}
     lens = _lengths(c)
+    if c["op"] == "attend":
+        pairs, keys = 0, 0
+        for n in lens:
+            see = _ranges(c) if c["docs"] or c["prefix"] else [(0, n)] * c["S"]
+            at = [n - c["S"] + i for i in range(c["S"])]
+            see = [(max(lo, p - c["window"] + 1) if c["window"] else lo, min(hi, p + 1) if c["causal"] else hi)
+                   for (lo, hi), p in zip(see, at)]
+            pairs += sum(max(0, hi - lo) for lo, hi in see)
+            keys += max(hi for _, hi in see) - min(lo for lo, _ in see)
+        qo, kv = c["B"] * c["h_q"] * c["S"], keys * c["h_kv"]
+        nbytes = (2 * qo + 2 * kv) * c["d"] * e + 4 * qo
+        if not c["grad"]:
+            return {"bytes": nbytes, "flops": 4 * pairs * c["h_q"] * c["d"]}
+        return {"bytes": nbytes + (2 * qo + 2 * c["B"] * c["T"] * c["h_kv"]) * c["d"] * e,
+                "flops": 14 * pairs * c["h_q"] * c["d"]}
     if c["op"] == "weights":
         pairs, keys = 0, 0
         for n in lens:
@@ -205,6 +261,22 @@ def prepare(c, seed):
         return s
     lens = torch.tensor(_lengths(c), dtype=torch.int32, device="cuda")
     s["lens"] = lens
+    if c["op"] == "attend":
+        # peaked scores (standard deviation 3), so that the cap and the bias matter
+        s["q"] = (3.0 * torch.randn((B, c["h_q"], c["S"], d), generator=g, device="cuda")).to(dt)
+        s["k"], s["v"] = normal(B, c["h_kv"], c["T"], d), normal(B, c["h_kv"], c["T"], d)
+        s["slopes"] = 2.0 ** (-8.0 * (1 + torch.arange(c["h_q"], device="cuda")) / c["h_q"]) if c["alibi"] else None
+        s["range"] = None
+        if c["docs"] or c["prefix"]:
+            s["range"] = torch.tensor(_ranges(c), dtype=torch.int32, device="cuda").expand(B, -1, -1).contiguous()
+        if c["grad"]:
+            s["do"] = normal(B, c["h_q"], c["S"], d)
+        if c["page"]:
+            s["k"], s["table"] = _pool(s["k"], c["page"], g)
+            s["v"] = torch.randn(s["k"].shape, generator=g, device="cuda").to(dt)
+        if c["S"] == 1 and not c["grad"]:
+            s["q"] = s["q"][:, :, 0].contiguous()
+        return s
     behind = torch.arange(c["T"], device="cuda")[None, :] >= lens[:, None]  # rows that hold nothing yet
     if c["op"] == "weights":
         k = normal(B, c["h_kv"], c["T"], d)
@@ -277,6 +349,49 @@ def _dense(pages, table):
     return pages[table.long()].transpose(1, 2).reshape(B, h, n * p, d)
 
 
+def _attended(s):
+    """Capped and biased attention over the keys each row sees, and its gradients."""
+    c = s["c"]
+    k, v = (_dense(s[n], s["table"]) if c["page"] else s[n] for n in ("k", "v"))
+    q = s["q"].float().reshape(c["B"], c["h_kv"], -1, c["d"])
+    k, v, scale = k.float()[:, :, :c["T"]], v.float(), 1 / math.sqrt(c["d"])
+    shape = (c["B"], c["h_kv"], c["h_q"] // c["h_kv"], c["S"], c["T"])
+    score = (q @ k.transpose(2, 3) * scale).view(shape)
+    if c["cap"]:
+        turn = torch.tanh(score / c["cap"])
+        score = c["cap"] * turn
+    at = (s["lens"][:, None] - c["S"] + torch.arange(c["S"], device="cuda"))[:, :, None]
+    key = torch.arange(c["T"], device="cuda")
+    if c["alibi"]:
+        away = (at - key).abs()[:, None, None]
+        score = score - s["slopes"].view(1, c["h_kv"], -1, 1, 1) * away
+    seen = key < s["lens"][:, None, None]
+    if c["causal"]:
+        seen = seen & (key <= at)
+    if c["window"]:
+        seen = seen & (key > at - c["window"])
+    if s["range"] is not None:
+        seen = seen & (key >= s["range"][..., :1]) & (key < s["range"][..., 1:])
+    score = score.masked_fill(~seen[:, None, None], float("-inf"))
+    lse = torch.logsumexp(score, -1)
+    p = (score - lse[..., None]).exp_()
+    flat = (c["B"], c["h_kv"], -1, c["T"])
+    o = p.reshape(flat) @ v
+    out = {"o": o.to(s["q"].dtype).view(s["q"].shape), "lse": lse.view(s["q"].shape[:-1])}
+    if not c["grad"]:
+        return out
+    do = s["do"].float().reshape(q.shape)
+    dp = (do @ v.transpose(2, 3) - (do * o).sum(-1, keepdim=True)).view(shape)
+    ds = p * dp
+    if c["cap"]:
+        ds = ds * (1 - turn * turn)
+    ds = ds.reshape(flat) * scale
+    out["dq"] = (ds @ k).to(s["q"].dtype).view(s["q"].shape)
+    out["dk"] = (ds.transpose(2, 3) @ q).to(s["q"].dtype)
+    out["dv"] = (p.reshape(flat).transpose(2, 3) @ do).to(s["q"].dtype)
+    return out
+
+
 def _plain(s):
     c = s["c"]
     if c["op"] == "rope":
@@ -294,6 +409,8 @@ def _plain(s):
         s["kc"][page, :, slot] = k
         s["vc"][page, :, slot] = v
         return {"q": q, "k": s["kc"], "v": s["vc"]}
+    if c["op"] == "attend":
+        return _attended(s)
     lens, T = s["lens"], c["T"]
     inside = torch.arange(T, device="cuda")[None, :] < lens[:, None]
     if c["op"] == "weights":
@@ -350,6 +467,19 @@ def _called(s):
         else:
             q = gqa.kv_rope_append(s["q"], s["k"], s["v"], s["kc"], s["vc"], s["pos"], s["inv_freq"], **how)
         return {"q": q, "k": s["kc"], "v": s["vc"]}
+    if c["op"] == "attend":
+        how = dict(kv_len=s["lens"], softcap=c["cap"], alibi_slopes=s["slopes"], key_range=s["range"],
+                   window=c["window"])
+        if s["q"].dim() == 3:
+            o, lse = (gqa.decode_paged(s["q"], s["k"], s["v"], s["table"], return_lse=True, **how) if c["page"]
+                      else gqa.decode(s["q"], s["k"], s["v"], return_lse=True, **how))
+            return {"o": o, "lse": lse}
+        how.update(q_start=s["lens"] - c["S"], causal=c["causal"])
+        o, lse = gqa.prefill(s["q"], s["k"], s["v"], return_lse=True, **how)
+        if not c["grad"]:
+            return {"o": o, "lse": lse}
+        dq, dk, dv = gqa.prefill_backward(s["q"], s["k"], s["v"], o, s["do"], lse, **how)
+        return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
     if c["op"] == "weights":
         how = dict(kv_len=s["lens"], window=c["window"], weights=s["w"] if c["accumulate"] else None)
         if c["page"]:
@@ -407,6 +537,46 @@ def exact(c, seed):
                 at, to = int(s["table"][b, (p + lo) // c["page"]]), (p + lo) % c["page"]
                 kc[at, :, to:to + hi - lo], vc[at, :, to:to + hi - lo] = k[:, lo:hi], s["v"][b, :, lo:hi].double()
         return {"q": torch.stack(q), "k": kc, "v": vc}
+    if c["op"] == "attend":
+        names = ("q", "k", "v") if c["grad"] else ()
+        outs = {n: [] for n in ("o", "lse", *("d" + n for n in names))}
+        for b, n in enumerate(_lengths(c)):
+            at = torch.arange(n - c["S"], n, device="cuda")[:, None]
+            key = torch.arange(c["T"], device="cuda")[None, :]
+            hidden = key >= n
+            if c["causal"]:
+                hidden = hidden | (key > at)
+            if c["window"]:
+                hidden = hidden | (at - key >= c["window"])
+            if s["range"] is not None:
+                hidden = hidden | (key < s["range"][b, :, :1]) | (key >= s["range"][b, :, 1:])
+            group = {m: [] for m in outs}
+            for g in range(c["h_kv"]):
+                k, v = (s[m][s["table"][b].long(), g].reshape(-1, c["d"]) if c["page"] else s[m][b, g] for m in ("k", "v"))
+                k, v = k.double(), v.double()
+                sums = [torch.zeros_like(k), torch.zeros_like(v)]
+                for a in range(g * c["h_q"] // c["h_kv"], (g + 1) * c["h_q"] // c["h_kv"]):
+                    x = [t.detach().requires_grad_(c["grad"])
+                         for t in (s["q"][b, a].reshape(c["S"], c["d"]).double(), k, v)]
+                    z = torch.einsum("id,jd->ij", x[0], x[1]) * c["d"] ** -0.5
+                    z = c["cap"] * torch.tanh(z / c["cap"]) if c["cap"] else z
+                    z = z - s["slopes"][a].double() * (at - key).abs() if c["alibi"] else z
+                    z = z.masked_fill(hidden, -math.inf)
+                    o = torch.softmax(z, -1) @ x[2]
+                    group["o"].append(o.detach())
+                    group["lse"].append(torch.logsumexp(z, -1).detach())
+                    if c["grad"]:
+                        dq, dk, dv = torch.autograd.grad(o, x, s["do"][b, a].double())
+                        group["dq"].append(dq)
+                        sums = [sums[0] + dk, sums[1] + dv]
+                if c["grad"]:
+                    group["dk"].append(sums[0])
+                    group["dv"].append(sums[1])
+            for m in outs:
+                outs[m].append(torch.stack(group[m]))
+        outs = {m: torch.stack(t) for m, t in outs.items()}
+        outs["o"], outs["lse"] = outs["o"].view(s["q"].shape), outs["lse"].view(s["q"].shape[:-1])
+        return outs
     if c["op"] == "weights":
         w = s["w"].double() if c["accumulate"] else torch.zeros(s["w"].shape, dtype=torch.float64, device="cuda")
         q = s["q"].reshape(B, c["h_q"], c["S"], c["d"]).double()
