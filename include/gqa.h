@@ -310,6 +310,63 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
                            gqa_dtype dtype, void* stream);
 
 /*
+ * gqa_rope - rotary position embedding of the rows x (B, h, S, d). Pair i of the d_rot elements from
+ * `offset` on turns by the angle p * inv_freq[i] of the row's position p; the other elements are
+ * copied. With c = scale * cos, s = scale * sin of the angle and m = d_rot / 2:
+ *   interleaved 0 (halves):     (x[i], x[m + i])       -> (x[i] c - x[m + i] s, x[m + i] c + x[i] s)
+ *   interleaved 1 (neighbours): (x[2 i], x[2 i + 1])   likewise, indices from `offset`.
+ * Angles are formed and reduced in 64 bits, the rotation is fp32, the result is rounded once.
+ * Position encoding is what prefill, decode and mla_decode expect of their queries and keys; the
+ * keys are rotated once, before they are cached.
+ *
+ *   x, out     rows of d elements, x != out or both the same memory with the same strides (in place).
+ *   inv_freq   device double[d_rot / 2]: radians per position. Context scaling is in these values
+ *              and in `scale` (finite; 1 for none).
+ *   positions  device int32: per_token 0: (B), token t of sequence b sits at positions[b] + t;
+ *              per_token 1: (B, S). A negative position: the row is written as zeros and
+ *              GQA_DEVERR_POSITION is set.
+ *   strides    HOST int64[3] of x and of out: elements between sequences, heads and tokens (the
+ *              elements of a row are adjacent), or NULL for dense (B, h, S, d). A fused q/k/v
+ *              projection (B, S, heads, d) is read in place this way.
+ *   inverse    1: rotate by the opposite angle. It is the transpose, so it maps the gradient of a
+ *              rotated row to the gradient of the row (same `scale`).
+ * S = 0 is a no-op. d_rot even, 0 < d_rot, offset + d_rot <= d <= 4096; B * S below 2^31.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gqa_status gqa_rope(const void* x, void* out, const double* inv_freq, const int32_t* positions,
+                    int per_token, int B, int h, int S, int d, int d_rot, int offset,
+                    const int64_t* x_strides, const int64_t* out_strides, int interleaved, int inverse,
+                    float scale, gqa_dtype dtype, void* stream);
+
+/*
+ * kv_rope_append, kv_rope_append_paged - gqa_rope of a step's q and k and kv_append of k and v, in one
+ * launch: q_out = rope(q); cache rows pos[b] + t of k_cache = rope(k_new), of v_cache = v_new.
+ *   q (B, h_q, S_new, d_h), k_new, v_new (B, h_kv, S_new, d_h) with strides as in gqa_rope (NULL:
+ *              dense); q_out dense (B, h_q, S_new, d_h), or q itself when q is dense.
+ *   pos        device int32[B]: first cache row written, as in kv_append. The errors are kv_append's:
+ *              a sequence that does not fit is not cached (GQA_DEVERR_POSITION), nor a row whose page
+ *              is outside the pool (GQA_DEVERR_PAGE); its q_out is written all the same.
+ *   positions  as in gqa_rope, or NULL: a token's position is its cache row (they differ once
+ *              kv_evict has shortened the cache). A token with a negative position is not cached.
+ * Caches, block table and the other arguments as kv_append(_paged) and gqa_rope.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gqa_status kv_rope_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                          void* k_cache, void* v_cache, const double* inv_freq, const int32_t* pos,
+                          const int32_t* positions, int per_token, int B, int h_q, int h_kv, int S_new,
+                          int T_max, int d_h, int d_rot, int offset, const int64_t* q_strides,
+                          const int64_t* k_strides, const int64_t* v_strides, int interleaved,
+                          float scale, gqa_dtype dtype, void* stream);
+gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                void* k_pages, void* v_pages, const double* inv_freq,
+                                const int32_t* pos, const int32_t* positions, int per_token,
+                                const int32_t* block_table, int B, int h_q, int h_kv, int S_new,
+                                int num_pages, int page_size, int max_pages, int d_h, int d_rot,
+                                int offset, const int64_t* q_strides, const int64_t* k_strides,
+                                const int64_t* v_strides, int interleaved, float scale,
+                                gqa_dtype dtype, void* stream);
+
+/*
  * gqa_get_device_error - synchronise `stream`, then read and clear the sticky device error word
  * of the current device. *code receives a GQA_DEVERR_* value. Returns GQA_ERR_DEVICE when the word
  * was non-zero, GQA_OK when it was zero, GQA_ERR_CUDA if the read failed.

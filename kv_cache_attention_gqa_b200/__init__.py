@@ -18,9 +18,13 @@ from ._lib import (  # noqa: F401
     get_device_error,
     kv_append,
     kv_append_paged,
+    kv_rope_append,
+    kv_rope_append_paged,
     mla_decode,
     prefill,
     prefill_backward,
+    rope,
+    rope_frequencies,
     status_string,
     version,
     workspace,

@@ -9,6 +9,7 @@ fallback: if the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -33,6 +34,7 @@ DEVERR_NAMES = {0: "none", 1: "kv_len out of range", 2: "position out of range",
 
 # name -> (restype, argtypes), mirroring include/gqa.h
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L3 = ctypes.POINTER(ctypes.c_int64)  # three strides (host memory)
 SIGNATURES = {
     "gqa_prefill": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P]),
     "gqa_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
@@ -47,6 +49,11 @@ SIGNATURES = {
     "gqa_mla_decode": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _Z, _I, _P]),
     "gqa_prefill_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                   _F, _I, _I, _I, _P, _Z, _P]),
+    "gqa_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _L3, _L3, _I, _I, _F, _I, _P]),
+    "kv_rope_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _L3, _L3,
+                            _L3, _I, _F, _I, _P]),
+    "kv_rope_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                  _I, _I, _L3, _L3, _L3, _I, _F, _I, _P]),
     "gqa_get_device_error": (_I, [ctypes.POINTER(_I), _P]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
     "gqa_version": (ctypes.c_char_p, []),
@@ -436,3 +443,167 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, d_v: int = 512, *, kv_len=N
         _ptr(q), _ptr(cache), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), B, h_q, T_max, d_qk, d_v,
         scale, dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
     return (out, lse) if return_lse else out
+
+
+def _on_device(*ts):
+    """Every tensor given is a CUDA tensor on the current device (as _need_cuda, for strided inputs)."""
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors must live on the current CUDA device "
+                             f"(cuda:{torch.cuda.current_device()}), not {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """A (B, heads, S, d) tensor whose rows have adjacent elements; the other strides are free."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have the dimensions (B, heads, S, d)")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent (last stride 1)")
+    return t
+
+
+def _strides(t: torch.Tensor):
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def _positions(positions, B: int, S: int, device, name: str):
+    """(device int32 tensor, 1 when it holds a position per token): (B, S) per token, else first positions (B)."""
+    if isinstance(positions, torch.Tensor) and positions.dim() == 2:
+        if tuple(positions.shape) != (B, S):
+            raise ValueError(f"{name} must be ({B},) first positions or ({B}, {S}) positions")
+        return positions.to(device=device, dtype=torch.int32).contiguous(), 1
+    return _int_vec(positions, B, device, name), 0
+
+
+def _inv_freq(inv_freq: torch.Tensor, d: int, offset: int, device) -> torch.Tensor:
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a 1-D float64 tensor (see rope_frequencies)")
+    if inv_freq.device != torch.device(device) or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous and live on the same device as the rows")
+    if inv_freq.numel() < 1 or offset < 0 or offset + 2 * inv_freq.numel() > d:
+        raise ValueError(f"the rotated segment [{offset}, {offset + 2 * inv_freq.numel()}) must lie in a row of {d}")
+    return inv_freq
+
+
+def rope_frequencies(d_rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda"):
+    """Angles per position of the d_rot / 2 pairs and the magnitude for ``rope``: (inv_freq float64
+    tensor, scale). Without scaling inv_freq[i] = base ** (-2 i / d_rot) and scale = 1. For contexts
+    ``factor`` times longer than ``original_length``:
+    ``linear`` divides every frequency by factor; ``ntk`` raises the base so that the slowest pair is
+    slowed by factor and the fastest is kept; ``yarn`` keeps pairs that turn at least beta_fast times over
+    the original length, divides those that turn at most beta_slow times, blends in between, and returns
+    scale = 0.1 ln(factor) + 1."""
+    if d_rot <= 0 or d_rot % 2:
+        raise ValueError("d_rot must be even and positive")
+    if not (base > 0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base must be positive and factor at least 1")
+    i = torch.arange(d_rot // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk" and d_rot > 2:
+        base = base * factor ** (d_rot / (d_rot - 2))
+    f = base ** (-2.0 * i / d_rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_length <= 0 or not beta_fast > beta_slow:
+            raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow")
+        turns = original_length * f / (2.0 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'ntk' or 'yarn'")
+    return f.to(device), scale
+
+
+def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions, *, offset: int = 0, interleaved: bool = False,
+         inverse: bool = False, scale: float = 1.0, out=None) -> torch.Tensor:
+    """Rotary positions of the rows x (B, h, S, d), any strides but the last: pair i of the
+    2 * len(inv_freq) elements from ``offset`` on turns by position * inv_freq[i] and is multiplied by
+    ``scale``; the other elements are copied. ``positions``: (B,) first positions or (B, S). Pairs are
+    elements i and i + len(inv_freq) of the segment, or neighbours (``interleaved``). ``inverse`` turns
+    back: it maps the gradient of the result to the gradient of x. Returns a contiguous tensor, or ``out``
+    (which may be x itself)."""
+    _on_device(x, inv_freq, out)
+    _rows(x, "x")
+    B, h, S, d = x.shape
+    dt = _dtype_code(x)
+    inv_freq = _inv_freq(inv_freq, d, offset, x.device)
+    if out is None:
+        out = torch.empty((B, h, S, d), dtype=x.dtype, device=x.device)
+    else:
+        _rows(_out(out, x.shape, x.dtype, x.device), "out")
+        if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
+            raise ValueError("out must not be a broadcast tensor")
+        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+            raise ValueError("in place, out must have the strides of x")
+    pos_t, per_token = _positions(positions, B, S, x.device, "positions")
+    _check("gqa_rope", _lib.gqa_rope(
+        _ptr(x), _ptr(out), _ptr(inv_freq), _ptr(pos_t), per_token, B, h, S, d, 2 * inv_freq.numel(), offset,
+        _strides(x), _strides(out), 1 if interleaved else 0, 1 if inverse else 0, scale, dt, _stream()))
+    return out
+
+
+def _rope_append(q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, positions, offset, q_out):
+    """Checks and arguments shared by kv_rope_append and kv_rope_append_paged."""
+    _need_cuda(k_cache, v_cache, q_out)
+    _on_device(q, k_new, v_new, inv_freq)
+    for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+        _rows(t, name)
+    B, h_q, S, dq = q.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("the K and V caches must have one shape")
+    if dq != d or tuple(k_new.shape) != (B, h_kv, S, d) or v_new.shape != k_new.shape:
+        raise ValueError("q must be (B, h_q, S, d) and k_new, v_new (B, h_kv, S, d)")
+    dt = _dtype_code(q)
+    if any(t.dtype != q.dtype for t in (k_new, v_new, k_cache, v_cache)):
+        raise TypeError("q, k_new, v_new and the caches must share one dtype")
+    inv_freq = _inv_freq(inv_freq, d, offset, q.device)
+    pos_t = _int_vec(pos, B, q.device, "pos")
+    if pos_t is None:
+        raise ValueError("pos must be given")
+    at, per_token = (None, 0) if positions is None else _positions(positions, B, S, q.device, "positions")
+    q_out = _out(q_out, (B, h_q, S, d), q.dtype, q.device)
+    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        raise ValueError("in place, q must be contiguous")
+    return B, h_q, S, dt, inv_freq, pos_t, at, per_token, q_out
+
+
+def kv_rope_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, pos, inv_freq: torch.Tensor, *, positions=None, offset: int = 0,
+                   interleaved: bool = False, scale: float = 1.0, q_out=None) -> torch.Tensor:
+    """``rope`` of a step's q (B, h_q, S, d) and k_new (B, h_kv, S, d), with ``kv_append`` of the rotated
+    k and of v_new at cache rows pos[b] + t (in place), in one launch; returns the rotated q (contiguous).
+    ``positions``: as in ``rope``; None: a token's position is its cache row."""
+    if k_cache.dim() != 4 or k_cache.shape[0] != q.shape[0]:
+        raise ValueError("the caches must be (B, h_kv, T_max, d)")
+    _, h_kv, T_max, d = k_cache.shape
+    B, h_q, S, dt, inv_freq, pos_t, at, per_token, q_out = _rope_append(
+        q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, positions, offset, q_out)
+    _check("kv_rope_append", _lib.kv_rope_append(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(inv_freq), _ptr(pos_t),
+        _ptr(at), per_token, B, h_q, h_kv, S, T_max, d, 2 * inv_freq.numel(), offset, _strides(q),
+        _strides(k_new), _strides(v_new), 1 if interleaved else 0, scale, dt, _stream()))
+    return q_out
+
+
+def kv_rope_append_paged(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                         v_pages: torch.Tensor, pos, block_table, inv_freq: torch.Tensor, *, positions=None,
+                         offset: int = 0, interleaved: bool = False, scale: float = 1.0,
+                         q_out=None) -> torch.Tensor:
+    """``kv_rope_append`` into a paged cache (pools and block table as in ``kv_append_paged``)."""
+    num_pages, h_kv, page_size, d = _pool_shape(k_pages, v_pages)
+    B, h_q, S, dt, inv_freq, pos_t, at, per_token, q_out = _rope_append(
+        q, k_new, v_new, k_pages, v_pages, h_kv, d, pos, inv_freq, positions, offset, q_out)
+    bt = _block_table(block_table, B, q.device)
+    _check("kv_rope_append_paged", _lib.kv_rope_append_paged(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _ptr(inv_freq), _ptr(pos_t),
+        _ptr(at), per_token, _ptr(bt), B, h_q, h_kv, S, num_pages, page_size, bt.shape[1], d, 2 * inv_freq.numel(),
+        offset, _strides(q), _strides(k_new), _strides(v_new), 1 if interleaved else 0, scale, dt, _stream()))
+    return q_out

@@ -193,6 +193,90 @@ gqa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
 }
 }  // namespace
 
+namespace {
+void rope_strides(long long* to, const int64_t* from, int B, int h, int S, int d) {
+  const long long dense[3] = {(long long)h * S * d, (long long)S * d, d};
+  const int size[3] = {B, h, S};
+  for (int i = 0; i < 3; ++i) to[i] = size[i] == 1 ? 0 : from ? (long long)from[i] : dense[i];
+}
+
+// Checks and fills the arguments of a rotation (rows x -> out); strides are host arrays of three, in
+// elements, or NULL for dense rows. The stride of a dimension of size 1 is never used: it is taken as
+// zero, so that it does not narrow the vectors.
+gqa_status rope_args(RopeArgs& a, const void* x, void* out, const double* inv_freq,
+                     const int32_t* positions, int per_token, int B, int h, int S, int d, int d_rot,
+                     int offset, const int64_t* xs, const int64_t* os, int interleaved, int inverse,
+                     float scale, gqa_dtype dtype) {
+  if (B <= 0 || h <= 0 || S < 0 || d <= 0 || offset < 0) return GQA_ERR_INVALID_ARG;
+  if (d_rot <= 0 || d_rot % 2 != 0 || (long long)offset + d_rot > d) return GQA_ERR_INVALID_ARG;
+  if ((per_token | 1) != 1 || (interleaved | 1) != 1 || (inverse | 1) != 1) return GQA_ERR_INVALID_ARG;
+  if (!isfinite(scale)) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_BF16 && dtype != GQA_FP32) return GQA_ERR_INVALID_ARG;
+  if (S > 0 && (!x || !out || !inv_freq || !positions)) return GQA_ERR_INVALID_ARG;
+  if (d > 4096 || (long long)B * S >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  a.x = x;
+  a.out = out;
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.per_token = per_token;
+  a.B = B;
+  a.h = h;
+  a.S = S;
+  a.d = d;
+  a.d_rot = d_rot;
+  a.offset = offset;
+  rope_strides(a.xs, xs, B, h, S, d);
+  rope_strides(a.os, os, B, h, S, d);
+  a.interleaved = interleaved;
+  a.inverse = inverse;
+  a.scale = scale;
+  return GQA_OK;
+}
+
+gqa_status rope_launch(RopeArgs& a, gqa_dtype dtype, void* stream) {
+  a.err = device_error_ptr();
+  const int sms = sm_count();
+  if (!a.err || sms <= 0) return GQA_ERR_CUDA;
+  return from_cuda(launch_rope(a, dtype, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Shared body of kv_rope_append and kv_rope_append_paged (block_table != nullptr, T_max = max_pages *
+// page_size, k_cache / v_cache the page pools).
+gqa_status rope_append_impl(const void* q, const void* k_new, const void* v_new, void* q_out,
+                            void* k_cache, void* v_cache, const double* inv_freq, const int32_t* pos,
+                            const int32_t* positions, int per_token, int B, int h_q, int h_kv, int S_new,
+                            int T_max, int d_h, int d_rot, int offset, const int64_t* qs,
+                            const int64_t* ks, const int64_t* vs, int interleaved, float scale,
+                            gqa_dtype dtype, void* stream, const int32_t* block_table, int max_pages,
+                            int page_size, int num_pages) {
+  if (!k_cache || !v_cache || h_kv <= 0 || T_max <= 0) return GQA_ERR_INVALID_ARG;
+  if (S_new > 0 && (!k_new || !v_new || !pos)) return GQA_ERR_INVALID_ARG;
+  RopeArgs a;
+  // without positions a token's position is its cache row
+  const gqa_status st = rope_args(a, q, q_out, inv_freq, positions ? positions : pos,
+                                  positions ? per_token : 0, B, h_q, S_new, d_h, d_rot, offset, qs, nullptr,
+                                  interleaved, 0, scale, dtype);
+  if (st != GQA_OK) return st;
+  if (S_new > T_max) return GQA_ERR_INVALID_ARG;
+  if ((long long)h_q + 2ll * h_kv >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  if (S_new == 0) return GQA_OK;  // nothing to rotate or copy
+  a.h_kv = h_kv;
+  a.k = k_new;
+  a.v = v_new;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  rope_strides(a.ks, ks, B, h_kv, S_new, d_h);
+  rope_strides(a.vs, vs, B, h_kv, S_new, d_h);
+  a.pos = pos;
+  a.T_max = T_max;
+  a.block_table = block_table;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  return rope_launch(a, dtype, stream);
+}
+}  // namespace
+
 extern "C" {
 
 const char* gqa_status_string(gqa_status s) {
@@ -546,6 +630,46 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   return from_cuda(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gqa_status gqa_rope(const void* x, void* out, const double* inv_freq, const int32_t* positions,
+                    int per_token, int B, int h, int S, int d, int d_rot, int offset,
+                    const int64_t* x_strides, const int64_t* out_strides, int interleaved, int inverse,
+                    float scale, gqa_dtype dtype, void* stream) {
+  if (h <= 0) return GQA_ERR_INVALID_ARG;
+  RopeArgs a;
+  const gqa_status st = rope_args(a, x, out, inv_freq, positions, per_token, B, h, S, d, d_rot, offset,
+                                  x_strides, out_strides, interleaved, inverse, scale, dtype);
+  if (st != GQA_OK || S == 0) return st;
+  return rope_launch(a, dtype, stream);
+}
+
+gqa_status kv_rope_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                          void* k_cache, void* v_cache, const double* inv_freq, const int32_t* pos,
+                          const int32_t* positions, int per_token, int B, int h_q, int h_kv, int S_new,
+                          int T_max, int d_h, int d_rot, int offset, const int64_t* q_strides,
+                          const int64_t* k_strides, const int64_t* v_strides, int interleaved,
+                          float scale, gqa_dtype dtype, void* stream) {
+  return rope_append_impl(q, k_new, v_new, q_out, k_cache, v_cache, inv_freq, pos, positions, per_token, B,
+                          h_q, h_kv, S_new, T_max, d_h, d_rot, offset, q_strides, k_strides, v_strides,
+                          interleaved, scale, dtype, stream, nullptr, 0, 0, 0);
+}
+
+gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                void* k_pages, void* v_pages, const double* inv_freq,
+                                const int32_t* pos, const int32_t* positions, int per_token,
+                                const int32_t* block_table, int B, int h_q, int h_kv, int S_new,
+                                int num_pages, int page_size, int max_pages, int d_h, int d_rot,
+                                int offset, const int64_t* q_strides, const int64_t* k_strides,
+                                const int64_t* v_strides, int interleaved, float scale,
+                                gqa_dtype dtype, void* stream) {
+  if (num_pages <= 0 || page_size <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
+  if (S_new > 0 && !block_table) return GQA_ERR_INVALID_ARG;
+  const long long T_max = (long long)max_pages * page_size;
+  if (T_max >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  return rope_append_impl(q, k_new, v_new, q_out, k_pages, v_pages, inv_freq, pos, positions, per_token, B,
+                          h_q, h_kv, S_new, (int)T_max, d_h, d_rot, offset, q_strides, k_strides, v_strides,
+                          interleaved, scale, dtype, stream, block_table, max_pages, page_size, num_pages);
 }
 
 }  // extern "C"

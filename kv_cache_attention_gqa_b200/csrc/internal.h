@@ -25,6 +25,33 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+// Rotary positions: rows x (B, h, S, d) -> out, and with h_kv > 0 the append of a step's k (rotated)
+// and v (copied) rows to the cache. Strides are in elements, of the dimensions (B, heads, S).
+struct RopeArgs {
+  const void* x;
+  void* out;
+  const double* inv_freq;    // (d_rot / 2)
+  const int32_t* positions;  // (B) first position of each sequence, or (B, S) when per_token
+  int per_token;
+  int B, h, S, d, d_rot, offset;
+  long long xs[3], os[3];
+  int interleaved, inverse;
+  float scale;
+  unsigned* err;
+  // the append (h_kv = 0: none)
+  int h_kv = 0;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  void* k_cache = nullptr;
+  void* v_cache = nullptr;
+  long long ks[3] = {0, 0, 0}, vs[3] = {0, 0, 0};
+  const int32_t* pos = nullptr;  // first cache row of each sequence
+  int T_max = 0;
+  const int32_t* block_table = nullptr;  // paged cache (see DecodeArgs)
+  int max_pages = 0, page_size = 0, num_pages = 0;
+};
+cudaError_t launch_rope(const RopeArgs& a, gqa_dtype dtype, int num_sms, cudaStream_t s);
+
 struct PrefillArgs {
   const void* q;
   const void* k;

@@ -31,6 +31,7 @@ from .kv_append_ref import kv_append_ref
 from .paged import gather_pages, paged_append_ref, paged_decode_ref
 from .backward import attention_backward_ref, softmax_backward_rowterm
 from .mla import mla_decode_ref, mla_explicit_ref
+from .rope import rope_ref
 from . import ledgers
 
 __all__ = [
@@ -50,5 +51,6 @@ __all__ = [
     "softmax_backward_rowterm",
     "mla_decode_ref",
     "mla_explicit_ref",
+    "rope_ref",
     "ledgers",
 ]
