@@ -108,7 +108,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need_cuda(*ts):
@@ -132,8 +132,7 @@ def _int_vec(x, B: int, device, name: str):
     """Device int32[B] from None / int / sequence / tensor (None stays None = library default)."""
     if x is None:
         return None
-    if (isinstance(x, torch.Tensor) and x.is_cuda and x.device == torch.device(device)
-            and x.dtype == torch.int32 and x.is_contiguous()):
+    if (isinstance(x, torch.Tensor) and x.is_cuda and x.device == device and x.dtype == torch.int32 and x.is_contiguous()):
         if x.numel() != B:
             raise ValueError(f"{name} must have {B} entries")
         return x
@@ -167,7 +166,9 @@ def _scale(scale) -> float:
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The raw handle of the current stream (torch.cuda.current_stream() builds an object around it, which
+    costs more than the launch of a small kernel)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def debug_expire_waits(enable: bool) -> None:
@@ -447,14 +448,14 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, d_v: int = 512, *, kv_len=N
 
 def _on_device(*ts):
     """Every tensor given is a CUDA tensor on the current device (as _need_cuda, for strided inputs)."""
+    dev = torch.cuda.current_device()
     for t in ts:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors must live on the current CUDA device "
-                             f"(cuda:{torch.cuda.current_device()}), not {t.device}")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must live on the current CUDA device (cuda:{dev}), not {t.device}")
 
 
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -479,11 +480,11 @@ def _positions(positions, B: int, S: int, device, name: str):
     return _int_vec(positions, B, device, name), 0
 
 
-def _inv_freq(inv_freq: torch.Tensor, d: int, offset: int, device) -> torch.Tensor:
+def _inv_freq(inv_freq: torch.Tensor, d: int, offset: int) -> torch.Tensor:
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a 1-D float64 tensor (see rope_frequencies)")
-    if inv_freq.device != torch.device(device) or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be contiguous and live on the same device as the rows")
+    if not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous")
     if inv_freq.numel() < 1 or offset < 0 or offset + 2 * inv_freq.numel() > d:
         raise ValueError(f"the rotated segment [{offset}, {offset + 2 * inv_freq.numel()}) must lie in a row of {d}")
     return inv_freq
@@ -534,7 +535,7 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions, *, offset: int = 0,
     _rows(x, "x")
     B, h, S, d = x.shape
     dt = _dtype_code(x)
-    inv_freq = _inv_freq(inv_freq, d, offset, x.device)
+    inv_freq = _inv_freq(inv_freq, d, offset)
     if out is None:
         out = torch.empty((B, h, S, d), dtype=x.dtype, device=x.device)
     else:
@@ -552,8 +553,9 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions, *, offset: int = 0,
 
 def _rope_append(q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, positions, offset, q_out):
     """Checks and arguments shared by kv_rope_append and kv_rope_append_paged."""
-    _need_cuda(k_cache, v_cache, q_out)
-    _on_device(q, k_new, v_new, inv_freq)
+    _on_device(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and (q_out is None or q_out.is_contiguous())):
+        raise ValueError("the caches and q_out must be contiguous (row-major)")
     for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         _rows(t, name)
     B, h_q, S, dq = q.shape
@@ -564,7 +566,7 @@ def _rope_append(q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, posi
     dt = _dtype_code(q)
     if any(t.dtype != q.dtype for t in (k_new, v_new, k_cache, v_cache)):
         raise TypeError("q, k_new, v_new and the caches must share one dtype")
-    inv_freq = _inv_freq(inv_freq, d, offset, q.device)
+    inv_freq = _inv_freq(inv_freq, d, offset)
     pos_t = _int_vec(pos, B, q.device, "pos")
     if pos_t is None:
         raise ValueError("pos must be given")
