@@ -367,6 +367,45 @@ gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_
                                 gqa_dtype dtype, void* stream);
 
 /*
+ * gqa_kv_weights, gqa_kv_weights_paged - the attention weight each cached key receives, from the
+ * queries and the lse of a forward call (gqa_prefill, gqa_decode, gqa_decode_paged):
+ *   weights[b, g, j] (+)= sum over the heads a of group g and the rows i that see key j of
+ *                         exp(scale q[b, a, i] . k[b, g, j] - lse[b, a, i]).
+ * Summed over j this gives r S_q (each row's softmax sums to one). It is what kv_evict ranks keys by.
+ *
+ *   q          (B, h_q, S_q, d_h) position-encoded queries; S_q = 1 for a decoded token.
+ *   k_cache    (B, h_kv, T_max, d_h), or the page pool (num_pages, h_kv, page_size, d_h) with its
+ *              block table, as in gqa_decode_paged (page_size a multiple of 16); rows j < kv_len[b]
+ *              are read, and only their pages' table entries.
+ *   lse        (B, h_q, S_q) fp32, natural log. A row with lse = -inf or NaN adds nothing (padding
+ *              rows of a batch are left out this way).
+ *   weights    (B, h_kv, T_max) fp32. accumulate 0: every entry is written, zero where no row sees
+ *              the key; accumulate 1: the sums are added to entries j < kv_len[b], the others are left.
+ *   q_start    device int32[B] or NULL: cache row of query row 0; NULL: the queries are the last S_q
+ *              cached rows, q_start[b] = kv_len[b] - S_q.
+ *   kv_len, scale, causal, window: as in gqa_prefill. A sequence whose length or start is out of
+ *              range is flagged (GQA_DEVERR_KV_LEN, GQA_DEVERR_POSITION) and adds nothing.
+ *   dtype      GQA_BF16: d_h 64 or 128 (tcgen05 kernel); GQA_FP32: d_h <= 256 (check mode).
+ *   workspace  at least gqa_kv_weights_workspace_size(...) bytes, 256-byte aligned, no initial
+ *              contents; the size is 0, and the workspace may be NULL, when the query rows of a key
+ *              are summed in one place. Calls that share a workspace must not overlap on the GPU.
+ * The sums run in a fixed order: the same call gives the same bits. 2^31 limits as in gqa_prefill;
+ * B * h_kv <= 65535. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+size_t gqa_kv_weights_workspace_size(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype);
+gqa_status gqa_kv_weights(const void* q, const void* k_cache, const float* lse, float* weights,
+                          const int32_t* q_start, const int32_t* kv_len, int B, int h_q, int h_kv,
+                          int S_q, int T_max, int d_h, float scale, int causal, int window,
+                          int accumulate, gqa_dtype dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float* lse, float* weights,
+                                const int32_t* q_start, const int32_t* kv_len,
+                                const int32_t* block_table, int B, int h_q, int h_kv, int S_q,
+                                int num_pages, int page_size, int max_pages, int d_h, float scale,
+                                int causal, int window, int accumulate, gqa_dtype dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * gqa_get_device_error - synchronise `stream`, then read and clear the sticky device error word
  * of the current device. *code receives a GQA_DEVERR_* value. Returns GQA_ERR_DEVICE when the word
  * was non-zero, GQA_OK when it was zero, GQA_ERR_CUDA if the read failed.

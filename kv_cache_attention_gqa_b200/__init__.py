@@ -20,6 +20,8 @@ from ._lib import (  # noqa: F401
     kv_append_paged,
     kv_rope_append,
     kv_rope_append_paged,
+    kv_weights,
+    kv_weights_paged,
     mla_decode,
     prefill,
     prefill_backward,

@@ -54,6 +54,10 @@ SIGNATURES = {
                             _L3, _I, _F, _I, _P]),
     "kv_rope_append_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                   _I, _I, _L3, _L3, _L3, _I, _F, _I, _P]),
+    "gqa_kv_weights_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "gqa_kv_weights": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _I, _P, _Z, _P]),
+    "gqa_kv_weights_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _I,
+                                  _P, _Z, _P]),
     "gqa_get_device_error": (_I, [ctypes.POINTER(_I), _P]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
     "gqa_version": (ctypes.c_char_p, []),
@@ -609,3 +613,64 @@ def kv_rope_append_paged(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         _ptr(at), per_token, _ptr(bt), B, h_q, h_kv, S, num_pages, page_size, bt.shape[1], d, 2 * inv_freq.numel(),
         offset, _strides(q), _strides(k_new), _strides(v_new), 1 if interleaved else 0, scale, dt, _stream()))
     return q_out
+
+
+def _weights_args(q, k, lse, h_kv, T_max, d, weights, kv_len, q_start, ws):
+    """Checks and arguments shared by kv_weights and kv_weights_paged. q and lse may lack the row dimension
+    (one decoded token)."""
+    _need_cuda(q, k, lse, weights)
+    if q.dim() not in (3, 4) or lse.shape != q.shape[:-1] or q.shape[-1] != d:
+        raise ValueError("q must be (B, h_q, S_q, d_h) or (B, h_q, d_h), and lse its rows")
+    B, h_q = q.shape[:2]
+    S = q.shape[2] if q.dim() == 4 else 1
+    dt = _dtype_code(q)
+    if k.dtype != q.dtype:
+        raise TypeError("q and the cache must share one dtype")
+    if lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    accumulate = weights is not None
+    weights = _out(weights, (B, h_kv, T_max), torch.float32, q.device)
+    kl = _int_vec(kv_len, B, q.device, "kv_len")
+    qs = _int_vec(q_start, B, q.device, "q_start")
+    key = ("weights", B, h_q, h_kv, S, T_max, dt, q.get_device())
+    need = _ws_sizes.get(key)
+    if need is None:
+        need = _ws_sizes[key] = _lib.gqa_kv_weights_workspace_size(B, h_q, h_kv, S, T_max, dt)
+    if ws is None and need:
+        # not the cached workspace: that one's zeroed header belongs to the decode calls
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return B, h_q, S, dt, int(accumulate), weights, kl, qs, ws, 0 if ws is None else _ws_bytes(ws)
+
+
+def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, *, q_start=None, kv_len=None,
+               scale: float | None = None, causal: bool = True, window: int = 0, weights=None,
+               ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention weight of every cached key, fp32 (B, h_kv, T_max): the sum over the group's heads and the
+    query rows that see it of exp(scale q.k - lse). q (B, h_q, S_q, d_h) with lse (B, h_q, S_q) as returned
+    by ``prefill``, or (B, h_q, d_h) with (B, h_q) by ``decode``. ``q_start`` None: the queries are the
+    last S_q cached rows. ``weights`` given: the sums are added to its entries j < kv_len, in place."""
+    if k_cache.dim() != 4 or k_cache.shape[0] != q.shape[0]:
+        raise ValueError("k_cache must be (B, h_kv, T_max, d_h)")
+    _, h_kv, T_max, d = k_cache.shape
+    B, h_q, S, dt, acc, weights, kl, qs, ws, nws = _weights_args(q, k_cache, lse, h_kv, T_max, d, weights, kv_len,
+                                                                 q_start, ws)
+    _check("gqa_kv_weights", _lib.gqa_kv_weights(
+        _ptr(q), _ptr(k_cache), _ptr(lse), _ptr(weights), _ptr(qs), _ptr(kl), B, h_q, h_kv, S, T_max, d,
+        _scale(scale), 1 if causal else 0, int(window), acc, dt, _ptr(ws), nws, _stream()))
+    return weights
+
+
+def kv_weights_paged(q: torch.Tensor, k_pages: torch.Tensor, block_table, lse: torch.Tensor, *, q_start=None,
+                     kv_len=None, scale: float | None = None, causal: bool = True, window: int = 0,
+                     weights=None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """``kv_weights`` over a paged cache (pool and block table as in ``decode_paged``); weights are
+    (B, h_kv, max_pages * page_size), by logical position."""
+    num_pages, h_kv, page_size, d = _pool_shape(k_pages, k_pages)
+    bt = _block_table(block_table, q.shape[0], q.device)
+    max_pages = bt.shape[1]
+    B, h_q, S, dt, acc, weights, kl, qs, ws, nws = _weights_args(q, k_pages, lse, h_kv, max_pages * page_size, d,
+                                                                 weights, kv_len, q_start, ws)
+    _check("gqa_kv_weights_paged", _lib.gqa_kv_weights_paged(
+        _ptr(q), _ptr(k_pages), _ptr(lse), _ptr(weights), _ptr(qs), _ptr(kl), _ptr(bt), B, h_q, h_kv, S, num_pages,
+        page_size, max_pages, d, _scale(scale), 1 if causal else 0, int(window), acc, dt, _ptr(ws), nws, _stream()))
+    return weights

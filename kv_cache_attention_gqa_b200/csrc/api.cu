@@ -275,6 +275,46 @@ gqa_status rope_append_impl(const void* q, const void* k_new, const void* v_new,
   a.num_pages = num_pages;
   return rope_launch(a, dtype, stream);
 }
+
+// Shared body of gqa_kv_weights and gqa_kv_weights_paged (block_table != nullptr, T_max = max_pages *
+// page_size, k the page pool).
+gqa_status kv_weights_impl(KvWeightsArgs a, gqa_dtype dtype, size_t workspace_bytes, void* stream) {
+  if (!a.q || !a.k || !a.lse || !a.w) return GQA_ERR_INVALID_ARG;
+  if (a.B <= 0 || a.h_q <= 0 || a.h_kv <= 0 || a.S_q <= 0 || a.T_max <= 0 || a.d_h <= 0) return GQA_ERR_INVALID_ARG;
+  if (a.h_q % a.h_kv != 0 || !valid_scale(a.scale)) return GQA_ERR_INVALID_ARG;
+  if ((a.causal | 1) != 1 || (a.accumulate | 1) != 1) return GQA_ERR_INVALID_ARG;
+  if (a.window < 0 || (a.window > 0 && a.causal != 1)) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_BF16 && dtype != GQA_FP32) return GQA_ERR_INVALID_ARG;
+  if (dtype == GQA_FP32 && a.d_h > 256) return GQA_ERR_UNSUPPORTED;
+  if (dtype == GQA_BF16 && a.d_h != 64 && a.d_h != 128) return GQA_ERR_UNSUPPORTED;
+  const long long k_rows = a.block_table ? (long long)a.num_pages * a.h_kv * a.page_size
+                                         : (long long)a.B * a.h_kv * a.T_max;
+  if (k_rows >= (1ll << 31) || (long long)a.B * a.h_kv * a.T_max >= (1ll << 31) ||
+      (long long)a.B * a.h_q * a.S_q >= (1ll << 31) || (long long)a.B * a.h_kv > 65535)
+    return GQA_ERR_UNSUPPORTED;
+  a.scale = resolve_scale(a.scale, a.d_h);
+  const int sms = sm_count();
+  if (sms <= 0) return GQA_ERR_CUDA;
+  const size_t need = kv_weights_workspace_bytes(a.B, a.h_q, a.h_kv, a.S_q, a.T_max, dtype, sms);
+  if (need > 0 && (!a.workspace || (reinterpret_cast<uintptr_t>(a.workspace) & 255u) || workspace_bytes < need))
+    return GQA_ERR_WORKSPACE;
+  a.err = device_error_ptr();
+  if (!a.err) return GQA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == GQA_FP32) return from_cuda(launch_kv_weights_fp32(a, s));
+  int P, H;
+  kv_weights_tile(a.h_q, a.h_kv, a.S_q, &P, &H);
+  CUtensorMap maps[2];
+  const uint64_t kdims[2] = {(uint64_t)a.d_h, (uint64_t)k_rows};
+  const uint64_t kstrides[1] = {(uint64_t)a.d_h * 2};
+  const uint32_t kbox[2] = {64, (uint32_t)kv_weights_sub(a.block_table != nullptr, a.page_size)};
+  const uint64_t qdims[3] = {(uint64_t)a.d_h, (uint64_t)a.S_q, (uint64_t)a.B * a.h_q};
+  const uint64_t qstrides[2] = {(uint64_t)a.d_h * 2, (uint64_t)a.S_q * a.d_h * 2};
+  const uint32_t qbox[3] = {64, (uint32_t)P, (uint32_t)H};
+  if (!encode_bf16(&maps[0], a.k, 2, kdims, kstrides, kbox) || !encode_bf16(&maps[1], a.q, 3, qdims, qstrides, qbox))
+    return GQA_ERR_CUDA;
+  return from_cuda(launch_kv_weights_bf16(a, maps, sms, s));
+}
 }  // namespace
 
 extern "C" {
@@ -670,6 +710,72 @@ gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_
   return rope_append_impl(q, k_new, v_new, q_out, k_pages, v_pages, inv_freq, pos, positions, per_token, B,
                           h_q, h_kv, S_new, (int)T_max, d_h, d_rot, offset, q_strides, k_strides, v_strides,
                           interleaved, scale, dtype, stream, block_table, max_pages, page_size, num_pages);
+}
+
+size_t gqa_kv_weights_workspace_size(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype) {
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || S_q <= 0 || T_max <= 0 || h_q % h_kv != 0) return 0;
+  return kv_weights_workspace_bytes(B, h_q, h_kv, S_q, T_max, dtype, sm_count());
+}
+
+gqa_status gqa_kv_weights(const void* q, const void* k_cache, const float* lse, float* weights,
+                          const int32_t* q_start, const int32_t* kv_len, int B, int h_q, int h_kv,
+                          int S_q, int T_max, int d_h, float scale, int causal, int window,
+                          int accumulate, gqa_dtype dtype, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  KvWeightsArgs a;
+  a.q = q;
+  a.k = k_cache;
+  a.lse = lse;
+  a.w = weights;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.S_q = S_q;
+  a.T_max = T_max;
+  a.d_h = d_h;
+  a.scale = scale;
+  a.causal = causal;
+  a.window = window;
+  a.accumulate = accumulate;
+  a.workspace = workspace;
+  return kv_weights_impl(a, dtype, workspace_bytes, stream);
+}
+
+gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float* lse, float* weights,
+                                const int32_t* q_start, const int32_t* kv_len,
+                                const int32_t* block_table, int B, int h_q, int h_kv, int S_q,
+                                int num_pages, int page_size, int max_pages, int d_h, float scale,
+                                int causal, int window, int accumulate, gqa_dtype dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!block_table || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0) return GQA_ERR_UNSUPPORTED;
+  const long long T_max = (long long)max_pages * page_size;
+  if (T_max >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  KvWeightsArgs a;
+  a.q = q;
+  a.k = k_pages;
+  a.lse = lse;
+  a.w = weights;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.S_q = S_q;
+  a.T_max = (int)T_max;
+  a.d_h = d_h;
+  a.scale = scale;
+  a.causal = causal;
+  a.window = window;
+  a.accumulate = accumulate;
+  a.workspace = workspace;
+  a.block_table = block_table;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  return kv_weights_impl(a, dtype, workspace_bytes, stream);
 }
 
 }  // extern "C"

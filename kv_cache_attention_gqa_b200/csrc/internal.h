@@ -52,6 +52,31 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, gqa_dtype dtype, int num_sms, cudaStream_t s);
 
+// Attention weight of the cached keys (kv_weights.cu).
+struct KvWeightsArgs {
+  const void* q;
+  const void* k;
+  const float* lse;
+  float* w;
+  const int32_t* q_start;  // nullptr: the queries are the last S_q cached positions
+  const int32_t* kv_len;
+  int B, h_q, h_kv, S_q, T_max, d_h;
+  float scale;
+  int causal, window, accumulate;
+  void* workspace;
+  const int32_t* block_table = nullptr;  // paged cache (see DecodeArgs)
+  int max_pages = 0, page_size = 0, num_pages = 0;
+  unsigned* err;
+};
+// positions (P) and heads (H) of the bf16 kernel's Q tile, and keys per K copy
+void kv_weights_tile(int h_q, int h_kv, int S_q, int* P, int* H);
+int kv_weights_sub(bool paged, int page_size);
+size_t kv_weights_workspace_bytes(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype, int num_sms);
+// tmaps: [0] K rows as a 2-D view (d_h, rows) with box (64, kv_weights_sub); [1] queries as a 3-D view
+// (d_h, S_q, B*h_q) with box (64, P, H); SWIZZLE_128B.
+cudaError_t launch_kv_weights_bf16(const KvWeightsArgs& a, const CUtensorMap* tmaps, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_weights_fp32(const KvWeightsArgs& a, cudaStream_t s);
+
 struct PrefillArgs {
   const void* q;
   const void* k;

@@ -32,6 +32,7 @@ from .paged import gather_pages, paged_append_ref, paged_decode_ref
 from .backward import attention_backward_ref, softmax_backward_rowterm
 from .mla import mla_decode_ref, mla_explicit_ref
 from .rope import rope_ref
+from .kv_weights import kv_weights_ref
 from . import ledgers
 
 __all__ = [
@@ -52,5 +53,6 @@ __all__ = [
     "mla_decode_ref",
     "mla_explicit_ref",
     "rope_ref",
+    "kv_weights_ref",
     "ledgers",
 ]
