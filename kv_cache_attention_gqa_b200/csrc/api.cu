@@ -302,17 +302,24 @@ gqa_status kv_weights_impl(KvWeightsArgs a, gqa_dtype dtype, size_t workspace_by
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == GQA_FP32) return from_cuda(launch_kv_weights_fp32(a, s));
-  int P, H;
-  kv_weights_tile(a.h_q, a.h_kv, a.S_q, &P, &H);
+  const KvWeightsTile t = kv_weights_tile(a.h_q, a.h_kv, a.S_q);
   CUtensorMap maps[2];
   const uint64_t kdims[2] = {(uint64_t)a.d_h, (uint64_t)k_rows};
-  const uint64_t kstrides[1] = {(uint64_t)a.d_h * 2};
+  const uint64_t strides[1] = {(uint64_t)a.d_h * 2};
   const uint32_t kbox[2] = {64, (uint32_t)kv_weights_sub(a.block_table != nullptr, a.page_size)};
-  const uint64_t qdims[3] = {(uint64_t)a.d_h, (uint64_t)a.S_q, (uint64_t)a.B * a.h_q};
-  const uint64_t qstrides[2] = {(uint64_t)a.d_h * 2, (uint64_t)a.S_q * a.d_h * 2};
-  const uint32_t qbox[3] = {64, (uint32_t)P, (uint32_t)H};
-  if (!encode_bf16(&maps[0], a.k, 2, kdims, kstrides, kbox) || !encode_bf16(&maps[1], a.q, 3, qdims, qstrides, qbox))
-    return GQA_ERR_CUDA;
+  if (!encode_bf16(&maps[0], a.k, 2, kdims, strides, kbox)) return GQA_ERR_CUDA;
+  bool ok;
+  if (t.small) {
+    const uint64_t qdims[2] = {(uint64_t)a.d_h, (uint64_t)a.B * a.h_q * a.S_q};
+    const uint32_t qbox[2] = {64, (uint32_t)t.rows};
+    ok = encode_bf16(&maps[1], a.q, 2, qdims, strides, qbox);
+  } else {
+    const uint64_t qdims[3] = {(uint64_t)a.d_h, (uint64_t)a.S_q, (uint64_t)a.B * a.h_q};
+    const uint64_t qstrides[2] = {(uint64_t)a.d_h * 2, (uint64_t)a.S_q * a.d_h * 2};
+    const uint32_t qbox[3] = {64, (uint32_t)t.P, (uint32_t)t.H};
+    ok = encode_bf16(&maps[1], a.q, 3, qdims, qstrides, qbox);
+  }
+  if (!ok) return GQA_ERR_CUDA;
   return from_cuda(launch_kv_weights_bf16(a, maps, sms, s));
 }
 }  // namespace

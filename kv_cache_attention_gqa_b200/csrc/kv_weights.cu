@@ -4,22 +4,33 @@
 // Mathematics. Given lse the softmax needs no further statistics, so the weight of a key is a plain sum
 // over query rows of exp2(c s - lse2) with c = scale log2 e. The probabilities are never stored.
 //
-// bf16 kernel: key-stationary on the tensor cores. A unit of work is 128 keys of one (sequence, KV head)
-// against the query rows that see them (all of them, or one of `parts` shares of them). The keys sit on
-// the 128 TMEM lanes, S^T = K Q^T (tcgen05.mma, A = K tile, B = Q tile, both K-major in shared memory), so
+// bf16, more than 32 query rows a group (prompts, windows of queries): key-stationary on the tensor cores.
+// A unit of work is 256 keys of one (sequence, KV head) against the query rows that see them (all of them,
+// or one of `parts` shares of them). The keys of a K tile sit on the 128 TMEM lanes, S^T = K Q^T (tcgen05.mma, A = K tile, B = Q tile, both K-major in shared memory), so
 // the sum over rows runs along the columns a thread reads of its own lane: no exchange between threads, no
-// atomics, the same result every time. A Q tile is kNQ columns: P positions (a power of two) of H heads.
-//   kNQ = 128: prompts and windows of queries. Bound by the exponentials (one per visible pair; 16 a clock
-//              and SM) next to the MMA (512 clocks a 128 x 128 x 128 tile). Two warpgroups take half of the
-//              columns of each tile; S^T is buffered four deep.
-//   kNQ = 32:  a few rows per group (one decoded token): one Q tile a unit, bound by reading K once.
+// atomics, the same result every time. A Q tile is up to 128 columns: P positions of H heads.
+// Bound by the exponentials (one per visible pair, 16 a clock and SM: 2048 clocks per 256 x 128 tile) and
+// the MMAs, which run at 1650 clocks per tile instead of 1024 because both operands come from shared memory
+// and fill its 128 bytes a clock by themselves. Four warpgroups: one per 128 keys and half of the columns;
+// S^T is buffered twice. Measured (B200): 32 heads over 8 KV heads, 4096 rows, causal, d = 128: 116 us, 590
+// TFLOP/s. Even tiles to two warpgroups and odd ones to the other two: 137 us (each pair waits for its only
+// buffer's MMA); a quarter to a half of the exponentials as polynomials on the multiply-add pipe: no gain;
+// 128 keys a unit: 109 to 150 us for twice the L2 reads of Q.
 // When the units are fewer than the SMs need, or uneven (causal), the query rows of a unit are cut into
 // `parts`, whose sums meet in a second launch in a fixed order.
 // The grid is persistent, one CTA per SM; all roles walk the same units:
-//   warp 0      producer: K tiles and Q tiles by TMA into two rings; -lse2 and position of each column
+//   warp 0      producer: K tiles and Q tiles by TMA into two rings
 //   warp 1      issues the MMAs
-//   warps 2...  one thread per key and warpgroup: exponentials and sums (compensated, so that thousands of
+//   warp 2      -lse2 and position of each column of a Q tile
+//   warps 4...  one thread per key and warpgroup: exponentials and sums (compensated, so that thousands of
 //               rows keep fp32 accuracy)
+//
+// bf16, up to 32 query rows a group (one decoded token): bound by reading K once. A producer warp streams
+// 128-key K tiles with the group's rows, eight warps take 16 keys of each tile: S = Q K^T by m16n8k16 MMAs
+// (16 or 32 query rows are too few for a tcgen05 tile: its 128 x 16 MMAs took 1200 clocks a K tile against
+// 1450 for the tile's bytes, 34 us for the case below), and the sum over rows is three shuffles. Measured:
+// 8 sequences of 8192 keys, 8 KV heads, 4 rows each, d = 128 (138 MB): 31.0 us, 4.5 TB/s; two groups of
+// eight warps taking tiles in turn: 32.8 us, so what is left is the start and the end of a launch this short.
 //
 // fp32 check mode: one thread per key, scalar FFMA.
 
@@ -32,8 +43,9 @@
 namespace gqa {
 namespace kw {
 
-constexpr int kBK = 128;  // keys of a unit (= TMEM lanes)
+constexpr int kBK = 128;  // keys of a K tile (= TMEM lanes)
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSeqTable = 1024;  // sequences whose length and first position are kept in shared memory
 constexpr int kFar = 0x7ffffffe;  // the position of a row that sees every key (no causal mask)
 constexpr int kUnitsPerSm = 12;   // units wanted per SM before query rows are cut into parts
 constexpr int kTilesPerPart = 4;  // a part holds at least this many Q tiles (of the fullest unit)
@@ -45,13 +57,15 @@ struct WArgs {
   const int32_t* kv_len;
   int B, h_q, h_kv, r, S_q, T_max;
   int P, H, hblocks, npb;  // Q tile: P positions x H heads; blocks of heads, of positions
-  int N;                   // columns of a Q tile (MMA N)
-  int nkt;                 // key tiles of a sequence
+  int N;                   // MMA columns of a Q tile: P H rounded up to 16 (the rest is masked)
+  int nkt;                 // units along the keys of a sequence
   int parts;
-  long long n_units;
+  int n_units;
+  FastDiv div_bg, div_nkt, div_parts, div_hkv, div_P;
   float sl2;
   int causal, window, accumulate;
-  float* part;  // (parts, B * h_kv, nkt * 128) partial sums, when parts > 1
+  float* part;  // (parts, B * h_kv, keys of all units) partial sums, when parts > 1
+  int part_keys;
   const int32_t* block_table;
   int max_pages, page_size, num_pages, sub;  // sub: keys per K copy (128, or 64 / 16 on a paged cache)
   unsigned* err;
@@ -74,7 +88,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// One unit: keys k0 .. k0 + 127 of (b, g), and the Q tiles t0 .. t1 - 1 of the list (head block, position
+// One unit: kKeys keys from k0 on of (b, g), and the Q tiles t0 .. t1 - 1 of the list (head block, position
 // block pb_lo + ...) of the tiles whose rows see any of them.
 struct Unit {
   int b, g, part, k0, kv, qs;
@@ -84,19 +98,37 @@ struct Unit {
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
 
-__device__ __forceinline__ Unit make_unit(const WArgs& a, long long idx) {
+// (kv_len, q_start) of a sequence
+__device__ __forceinline__ int2 sequence(const WArgs& a, int b) {
+  const int kv = a.kv_len ? a.kv_len[b] : a.T_max;
+  return make_int2(kv, a.q_start ? a.q_start[b] : kv - a.S_q);
+}
+
+// seq: the first kSeqTable sequences' lengths and positions (a global load is a trip to L2 here, ~600
+// clocks in every role: shared memory leaves no L1).
+// kStream (the small kernel): key tiles fastest, so that the SMs together read the cache in its order.
+template <int kKeys, bool kStream = false>
+__device__ __forceinline__ Unit make_unit(const WArgs& a, const int2* seq, int idx) {
   Unit u;
-  // key tiles slowest: the tiles that most rows see (causal) come first, and a CTA's units spread over
-  // the sequences
-  const int bg_n = a.B * a.h_kv;
-  const int kp = (int)(idx / bg_n), bg = (int)(idx - (long long)kp * bg_n);
-  const int kt = kp / a.parts;
-  u.part = kp - kt * a.parts;
-  u.b = bg / a.h_kv;
+  int kt, bg;
+  if constexpr (kStream) {
+    bg = a.div_nkt.div(idx);
+    kt = idx - bg * a.nkt;
+    u.part = 0;
+  } else {
+    // key tiles slowest: the tiles that most rows see (causal) come first, and a CTA's units spread over
+    // the sequences
+    const int kp = a.div_bg.div(idx);
+    bg = idx - kp * (a.B * a.h_kv);
+    kt = a.div_parts.div(kp);
+    u.part = kp - kt * a.parts;
+  }
+  u.b = a.div_hkv.div(bg);
   u.g = bg - u.b * a.h_kv;
-  u.k0 = kt * kBK;
-  u.kv = a.kv_len ? a.kv_len[u.b] : a.T_max;
-  u.qs = a.q_start ? a.q_start[u.b] : u.kv - a.S_q;
+  u.k0 = kt * kKeys;
+  const int2 sq = u.b < kSeqTable ? seq[u.b] : sequence(a, u.b);
+  u.kv = sq.x;
+  u.qs = sq.y;
   u.valid = u.kv >= 1 && u.kv <= a.T_max && u.qs >= 0;
   u.pb_lo = u.npb = u.t0 = u.t1 = 0;
   if (!u.valid || u.k0 >= u.kv) return u;
@@ -104,16 +136,16 @@ __device__ __forceinline__ Unit make_unit(const WArgs& a, long long idx) {
   if (a.causal) {
     if (u.k0 - u.qs > 0) i_lo = u.k0 - u.qs;
     if (a.window > 0) {
-      const long long hi = (long long)min(u.k0 + kBK, u.kv) - 1 + a.window - 1 - u.qs;
+      const long long hi = (long long)min(u.k0 + kKeys, u.kv) - 1 + a.window - 1 - u.qs;
       if (hi < i_hi) i_hi = (int)(hi < -1 ? -1 : hi);
     }
   }
   if (i_lo > i_hi) return u;
-  u.pb_lo = i_lo / a.P;
-  u.npb = i_hi / a.P - u.pb_lo + 1;
-  const long long n = (long long)u.npb * a.hblocks;
-  u.t0 = (int)(n * u.part / a.parts);
-  u.t1 = (int)(n * (u.part + 1) / a.parts);
+  u.pb_lo = a.div_P.div(i_lo);
+  u.npb = a.div_P.div(i_hi) - u.pb_lo + 1;
+  const int n = u.npb * a.hblocks;  // times parts below 2^31 (the host bounds the list by it)
+  u.t0 = a.div_parts.div(n * u.part);
+  u.t1 = a.div_parts.div(n * (u.part + 1));
   return u;
 }
 
@@ -123,23 +155,29 @@ __device__ __forceinline__ long long unit_of(int it) {
   return base + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-template <int D, int kNQ>
+constexpr int kNQ = 128;  // columns of a Q tile
+
+template <int D>
 struct Cfg {
   static constexpr int kNch = D / 64;
-  static constexpr int kWG = kNQ == 128 ? 2 : 1;  // epilogue warpgroups
-  static constexpr int kThreads = 64 + 128 * kWG;
-  static constexpr int kKStages = kNQ == 128 ? 2 : 5;
-  static constexpr int kQStages = kNQ == 128 ? 4 : 5;
-  static constexpr int kBufs = kNQ == 128 ? 4 : 8;  // S^T buffers in TMEM and their column statistics
-  static constexpr uint32_t kTmemCols = kBufs * kNQ;
+  static constexpr int kWG = 4;  // warpgroups of exponentials
+  static constexpr int kKT = 2;  // K tiles of a unit
+  static constexpr int kKeys = kKT * kBK;
+  static constexpr int kThreads = 128 + 128 * kWG;
+  static constexpr int kKStages = 3;
+  static constexpr int kQStages = 3;
+  static constexpr int kBufs = 2;  // S^T buffers in TMEM and their column statistics
+  static constexpr uint32_t kBufCols = kKT * kNQ;  // one buffer: a tile of scores per K tile
+  static constexpr uint32_t kTmemCols = kBufs * kBufCols;
   static constexpr int kKChunk = kBK * 128, kKBytes = kNch * kKChunk;
-  static constexpr int kQChunkMax = kNQ * 128, kQBytes = kNch * kQChunkMax;
+  static constexpr int kQChunk = kNQ * 128, kQBytes = kNch * kQChunk;
   static constexpr int kOffQ = kKStages * kKBytes;
   static constexpr int kOffStat = kOffQ + kQStages * kQBytes;
   // per buffer: -lse2 of the columns, their positions, and (min, max) position of each 32 columns
   static constexpr int kStatWords = 2 * kNQ + 2 * (kNQ / 32);
-  static constexpr int kOffX = kOffStat + kBufs * kStatWords * 4;  // second warpgroup's sums, two units
-  static constexpr int kOffBar = kOffX + (kWG == 2 ? 2 * 128 * 4 : 0);
+  static constexpr int kOffX = kOffStat + kBufs * kStatWords * 4;  // sums over the second columns, two units
+  static constexpr int kOffSeq = kOffX + 2 * kKeys * 4;
+  static constexpr int kOffBar = kOffSeq + kSeqTable * 8;
   static constexpr int kSmemRaw = kOffBar + 512 + 1024;
   // at least half of an SM's shared memory: one CTA per SM (it allocates up to all TMEM columns)
   static constexpr int kSmem = kSmemRaw > 120 * 1024 ? kSmemRaw : 120 * 1024;
@@ -152,11 +190,11 @@ struct Cfg {
   static_assert(kBars * 8 + 16 <= 512, "barrier block");
 };
 
-template <int D, int kNQ>
-__global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     kv_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ WArgs a) {
-  using C = Cfg<D, kNQ>;
+  using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -186,13 +224,15 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
       mbar_init(bar(C::bFree + i), 4 * C::kWG);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::bX + i), 128);
-      mbar_init(bar(C::bY + i), 128);
+      mbar_init(bar(C::bX + i), 256);
+      mbar_init(bar(C::bY + i), 256);
     }
     mbar_init(bar(C::bDone), 1);
     *abort = 0;
     fence_barrier_init();
   }
+  int2* seq = reinterpret_cast<int2*>(smem + C::kOffSeq);
+  for (int b = threadIdx.x; b < min(a.B, kSeqTable); b += C::kThreads) seq[b] = sequence(a, b);
   if (warp == 1) {
     tc::tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tc::tmem_relinquish();
@@ -201,7 +241,6 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
   cta_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int q_chunk = a.N * 128;  // bytes of one 64-column chunk of a Q tile
 
   if (warp == 0) {
     // ------------------------------ producer ------------------------------------------------
@@ -214,18 +253,20 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
     for (int it = 0; ok; ++it) {
       const long long idx = unit_of(it);
       if (idx >= a.n_units) break;
-      const Unit u = make_unit(a, idx);
+      const Unit u = make_unit<C::kKeys>(a, seq, (int)idx);
       if (!u.valid && u.k0 == 0 && u.part == 0 && u.g == 0 && lane == 0)
         set_device_error(a.err, u.kv < 1 || u.kv > a.T_max ? GQA_DEVERR_KV_LEN : GQA_DEVERR_POSITION);
       if (u.n() == 0) continue;
-      // K tile: one copy per 64-column chunk and sub-tile that holds cached keys
-      {
+      // K tiles that hold cached keys: one copy per 64-column chunk and sub-tile that holds any
+      const int n_kt = min(C::kKT, (u.kv - u.k0 + kBK - 1) / kBK);
+      for (int kt = 0; kt < n_kt; ++kt, ++nk) {
         const int st = nk % C::kKStages, f = nk / C::kKStages;
-        const int n_sub = (min(kBK, u.kv - u.k0) + a.sub - 1) / a.sub;
+        const int k0 = u.k0 + kt * kBK;
+        const int n_sub = (min(kBK, u.kv - k0) + a.sub - 1) / a.sub;
         int row = 0;
         if (a.block_table) {
           if (lane < n_sub) {
-            const int key = u.k0 + lane * a.sub;
+            const int key = k0 + lane * a.sub;
             int page = __ldg(a.block_table + (long long)u.b * a.max_pages + key / a.page_size);
             if (page < 0 || page >= a.num_pages) {
               set_device_error(a.err, GQA_DEVERR_PAGE);
@@ -234,7 +275,7 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
             row = (page * a.h_kv + u.g) * a.page_size + key % a.page_size;
           }
         } else {
-          row = (u.b * a.h_kv + u.g) * a.T_max + u.k0;
+          row = (u.b * a.h_kv + u.g) * a.T_max + k0;
         }
         if (lane == 0) {
           if (f > 0) ok = wait_bar(bar(C::bKEmpty + st), (uint32_t)((f - 1) & 1), abort, a.err);
@@ -248,57 +289,25 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
             tma_load_2d(sK + st * C::kKBytes + ch * C::kKChunk + lane * a.sub * 128, &tmk,
                         bar(C::bKFull + st), ch * 64, row);
         }
-        ++nk;
       }
-      for (int t = u.t0; t < u.t1; ++t, ++nt) {
-        const int hb = t / u.npb, pb = u.pb_lo + t - hb * u.npb;
-        const int head0 = u.g * a.r + hb * a.H, i0 = pb * a.P;
-        // statistics of this lane's columns: the loads are on their way before the ring is waited for
-        constexpr int kPer = kNQ / 32;
-        float l[kPer];
-        int ps[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const int n = e * 32 + lane;
-          const int h = n / a.P, i = i0 + n - h * a.P;
-          const bool in = n < a.N && hb * a.H + h < a.r && i < a.S_q;
-          l[e] = in ? __ldg(a.lse + ((long long)u.b * a.h_q + head0 + h) * a.S_q + i) : -INFINITY;
-          ps[e] = a.causal ? (int)min((long long)u.qs + i, (long long)kFar) : kFar;
-        }
-        const int st = nt % C::kQStages, f = nt / C::kQStages;
-        if (lane == 0) {
+      if (!ok) break;
+      if (lane == 0) {
+        int hb = u.t0 / u.npb, pb = u.t0 - hb * u.npb;
+        for (int t = u.t0; t < u.t1; ++t, ++nt) {
+          const int st = nt % C::kQStages, f = nt / C::kQStages;
           if (f > 0) ok = wait_bar(bar(C::bQEmpty + st), (uint32_t)((f - 1) & 1), abort, a.err);
-          if (ok) {
-            mbar_arrive_expect_tx(bar(C::bQFull + st), (uint32_t)(C::kNch * q_chunk));
-            for (int ch = 0; ch < C::kNch; ++ch)
-              tma_load_3d(sQ + st * C::kQBytes + ch * q_chunk, &tmq, bar(C::bQFull + st), ch * 64, i0,
-                          u.b * a.h_q + head0);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(C::bQFull + st), (uint32_t)(C::kNch * a.P * a.H * 128));
+          for (int ch = 0; ch < C::kNch; ++ch)
+            tma_load_3d(sQ + st * C::kQBytes + ch * C::kQChunk, &tmq, bar(C::bQFull + st), ch * 64,
+                        (u.pb_lo + pb) * a.P, u.b * a.h_q + u.g * a.r + hb * a.H);
+          if (++pb == u.npb) {
+            pb = 0;
+            ++hb;
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const int bf = nt % C::kBufs, fb = nt / C::kBufs;
-        if (lane == 0 && fb > 0) ok = wait_bar(bar(C::bFree + bf), (uint32_t)((fb - 1) & 1), abort, a.err);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          ++nt;
-          break;
-        }
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          // a row without a finite lse (no visible key, padding) takes part in nothing
-          const bool in = l[e] != -INFINITY && l[e] == l[e];
-          const int pos = in ? ps[e] : -1;
-          nl2(bf)[e * 32 + lane] = in ? -l[e] * kLog2e : 0.f;
-          cpos(bf)[e * 32 + lane] = pos;
-          const int lo = __reduce_min_sync(0xffffffffu, pos), hi = __reduce_max_sync(0xffffffffu, pos);
-          if (lane == 0) {
-            crange(bf)[2 * e] = lo;
-            crange(bf)[2 * e + 1] = hi;
-          }
-        }
-        mbar_arrive(bar(C::bStat + bf));
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     // drain (bounded): no copy may still land in shared memory at exit
     if (lane == 0) {
@@ -322,11 +331,12 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
     for (int it = 0; ok; ++it) {
       const long long idx = unit_of(it);
       if (idx >= a.n_units) break;
-      const Unit u = make_unit(a, idx);
+      const Unit u = make_unit<C::kKeys>(a, seq, (int)idx);
       if (u.n() == 0) continue;
-      const int ks = nk % C::kKStages;
-      if (!(ok = wait(C::bKFull + ks, (uint32_t)((nk / C::kKStages) & 1)))) break;
-      const uint64_t kd = dK + (uint64_t)((ks * C::kKBytes) >> 4);
+      const int n_kt = min(C::kKT, (u.kv - u.k0 + kBK - 1) / kBK);
+      for (int kt = 0; kt < n_kt && ok; ++kt)
+        ok = wait(C::bKFull + (nk + kt) % C::kKStages, (uint32_t)(((nk + kt) / C::kKStages) & 1));
+      if (!ok) break;
       for (int t = u.t0; t < u.t1; ++t, ++nt) {
         const int st = nt % C::kQStages, bf = nt % C::kBufs, fb = nt / C::kBufs;
         ok = wait(C::bQFull + st, (uint32_t)((nt / C::kQStages) & 1)) &&
@@ -335,38 +345,99 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
         tc::fence_after_sync();
         const uint64_t qd = dQ + (uint64_t)((st * C::kQBytes) >> 4);
         if (tc::elect_one()) {
+          for (int kt = 0; kt < n_kt; ++kt) {
+            const uint64_t kd = dK + (uint64_t)((((nk + kt) % C::kKStages) * C::kKBytes) >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_ss(tmem + bf * kNQ, kd + tc::koff(k, C::kKChunk), qd + tc::koff(k, q_chunk), idesc,
-                       k > 0 ? 1u : 0u);
+            for (int k = 0; k < D / 16; ++k)
+              tc::mma_ss(tmem + bf * C::kBufCols + kt * kNQ, kd + tc::koff(k, C::kKChunk), qd + tc::koff(k, C::kQChunk),
+                         idesc, k > 0 ? 1u : 0u);
+          }
           tc::commit(bar(C::bS + bf));
           tc::commit(bar(C::bQEmpty + st));
-          if (t + 1 == u.t1) tc::commit(bar(C::bKEmpty + ks));
+          if (t + 1 == u.t1)
+            for (int kt = 0; kt < n_kt; ++kt) tc::commit(bar(C::bKEmpty + (nk + kt) % C::kKStages));
         }
         __syncwarp();
       }
-      ++nk;
+      nk += n_kt;
     }
     if (tc::elect_one()) tc::commit(bar(C::bDone));
     __syncwarp();
     volatile int no_abort = 0;
     wait_bar(bar(C::bDone), 0, &no_abort, a.err);
-  } else {
+  } else if (warp == 2) {
+    // ------------------------------ column statistics ---------------------------------------
+    constexpr int kPer = kNQ / 32;
+    int hn[kPer], pn[kPer];  // head and position of this lane's columns inside a tile
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int n = e * 32 + lane;
+      hn[e] = n / a.P;
+      pn[e] = n - hn[e] * a.P;
+    }
+    int nt = 0, ok = 1;
+    for (int it = 0; ok; ++it) {
+      const long long idx = unit_of(it);
+      if (idx >= a.n_units) break;
+      const Unit u = make_unit<C::kKeys>(a, seq, (int)idx);
+      if (u.n() == 0) continue;
+      int hb = u.t0 / u.npb, pb = u.t0 - hb * u.npb;
+      for (int t = u.t0; t < u.t1; ++t, ++nt) {
+        float l[kPer];
+        int ps[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const int h = hb * a.H + hn[e], i = (u.pb_lo + pb) * a.P + pn[e];
+          const bool in = hn[e] < a.H && h < a.r && i < a.S_q;
+          l[e] = in ? __ldg(a.lse + ((long long)u.b * a.h_q + u.g * a.r + h) * a.S_q + i) : -INFINITY;
+          ps[e] = a.causal ? (int)min((long long)u.qs + i, (long long)kFar) : kFar;
+        }
+        if (++pb == u.npb) {
+          pb = 0;
+          ++hb;
+        }
+        const int bf = nt % C::kBufs, fb = nt / C::kBufs;
+        if (lane == 0 && fb > 0) ok = wait_bar(bar(C::bFree + bf), (uint32_t)((fb - 1) & 1), abort, a.err);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          // a row without a finite lse (no visible key, padding) takes part in nothing
+          const bool in = l[e] != -INFINITY && l[e] == l[e];
+          const int pos = in ? ps[e] : -1;
+          nl2(bf)[e * 32 + lane] = in ? -l[e] * kLog2e : 0.f;
+          cpos(bf)[e * 32 + lane] = pos;
+          const int lo = __reduce_min_sync(0xffffffffu, pos), hi = __reduce_max_sync(0xffffffffu, pos);
+          if (lane == 0) {
+            crange(bf)[2 * e] = lo;
+            crange(bf)[2 * e + 1] = hi;
+          }
+        }
+        mbar_arrive(bar(C::bStat + bf));
+      }
+    }
+  } else if (warp >= 4) {
     // ------------------------------ exponentials and sums: one key per thread ---------------
-    const int wg = (warp - 2) >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane;  // TMEM lane = key of the unit
-    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int wg = (warp >> 2) - 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // TMEM lane = key of the K tile
+    const int kh = wg >> 1, ch = wg & 1;  // K tile and half of the columns of this warpgroup
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16) + kh * kNQ;
     float* xs = reinterpret_cast<float*>(smem + C::kOffX);
-    constexpr int kCols = kNQ / C::kWG;  // columns of this warpgroup
-    const int col0 = wg * kCols;
-    int nt = 0, nu = 0;
+    const int reach = a.window > 0 ? a.window : 0x7fffffff;
+    int nt = 0, nu = 0;            // Q tiles and units with any so far
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const long long idx = unit_of(it);
       if (idx >= a.n_units) break;
-      const Unit u = make_unit(a, idx);
-      const int key = u.k0 + row;
-      float sum = 0.f, comp = 0.f;  // compensated sum of the 32-column sums
+      const Unit u = make_unit<C::kKeys>(a, seq, (int)idx);
+      const int k0 = u.k0 + kh * kBK, key = k0 + row;
+      const long long bg = (long long)u.b * a.h_kv + u.g;
+      const bool writes = ch == 0;
+      const bool in = u.valid && key < u.kv;
+      float* const dst = a.w + bg * a.T_max + key;
+      // the entry to be added to is loaded ahead of the sum
+      const float old = writes && a.accumulate && a.parts == 1 && in && u.n() > 0 ? *dst : 0.f;
+      float sum = 0.f, comp = 0.f;  // compensated sum of the column groups' sums
       for (int t = u.t0; t < u.t1; ++t, ++nt) {
         const int bf = nt % C::kBufs;
         const uint32_t ph = (uint32_t)((nt / C::kBufs) & 1);
@@ -374,36 +445,41 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
+        const float2 c2 = make_float2(a.sl2, a.sl2);
 #pragma unroll
-        for (int cc = 0; cc < kCols / 32; ++cc) {
-          const int c0 = col0 + cc * 32;
-          const int lo = crange(bf)[2 * (c0 / 32)], hi = crange(bf)[2 * (c0 / 32) + 1];
-          if (hi < u.k0) continue;  // no column of these sees any of the keys
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c0 = ch * 64 + cc * 32;
+          const int lo = crange(bf)[c0 / 16], hi = crange(bf)[c0 / 16 + 1];
+          if (hi < k0 || k0 >= u.kv) continue;  // no column sees one of the keys, or there are none
           float s[32];
-          tc::ld32f(lane_addr + bf * kNQ + c0, s);
+          tc::ld32f(lane_addr + bf * C::kBufCols + c0, s);
           tc::wait_ld();
-          const bool all = lo >= u.k0 + kBK - 1 && (a.window == 0 || u.k0 > hi - a.window);
+          const bool all = lo >= k0 + kBK - 1 && (a.window == 0 || k0 > hi - a.window);
           const float* nl = nl2(bf) + c0;
-          float s0 = 0.f, s1 = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+          auto expo = [&](int k, float2 n) {
+            const float2 x = pair_fma(make_float2(s[k], s[k + 1]), c2, n);
+            return make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          };
           if (all) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              s0 += fast_exp2(fmaf(s[k], a.sl2, nl[k]));
-              s1 += fast_exp2(fmaf(s[k + 1], a.sl2, nl[k + 1]));
+            for (int k = 0; k < 32; k += 4) {
+              const float4 n = *reinterpret_cast<const float4*>(nl + k);
+              acc = pair_add(acc, expo(k, make_float2(n.x, n.y)));
+              acc = pair_add(acc, expo(k + 2, make_float2(n.z, n.w)));
             }
           } else {
-            const int* cp = cpos(bf) + c0;
-            const int reach = a.window > 0 ? a.window : 0x7fffffff;
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
+              float2 p = expo(k, *reinterpret_cast<const float2*>(nl + k));
               // key <= position, and within the window: position - key < window
-              const bool v0 = key <= cp[k] && cp[k] - key < reach;
-              const bool v1 = key <= cp[k + 1] && cp[k + 1] - key < reach;
-              s0 += v0 ? fast_exp2(fmaf(s[k], a.sl2, nl[k])) : 0.f;
-              s1 += v1 ? fast_exp2(fmaf(s[k + 1], a.sl2, nl[k + 1])) : 0.f;
+              const int2 at = *reinterpret_cast<const int2*>(cpos(bf) + c0 + k);
+              if (key > at.x || at.x - key >= reach) p.x = 0.f;
+              if (key > at.y || at.y - key >= reach) p.y = 0.f;
+              acc = pair_add(acc, p);
             }
           }
-          const float y = (s0 + s1) - comp, tot = sum + y;
+          const float y = (acc.x + acc.y) - comp, tot = sum + y;
           comp = (tot - sum) - y;
           sum = tot;
         }
@@ -412,34 +488,28 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar(C::bFree + bf));
       }
       if (!ok) break;
-      if (C::kWG == 2 && u.n() > 0) {
-        // the second warpgroup hands its sums to the first (two units may be under way)
+      if (u.n() > 0) {
+        // the sums over the second columns join the first (two units may be under way)
         const int sl = nu & 1;
         const uint32_t ph = (uint32_t)((nu >> 1) & 1);
-        if (wg == 1) {
+        float* x = xs + sl * C::kKeys + kh * kBK + row;
+        if (ch == 1) {
           if (nu >= 2) ok = wait_bar(bar(C::bY + sl), ph ^ 1u, abort, a.err);
-          xs[sl * 128 + row] = sum;
+          *x = sum;
           mbar_arrive(bar(C::bX + sl));
         } else {
           ok = wait_bar(bar(C::bX + sl), ph, abort, a.err);
-          sum += xs[sl * 128 + row];
+          sum += *x;
           mbar_arrive(bar(C::bY + sl));
         }
         ok = __all_sync(0xffffffffu, ok);
-        ++nu;
         if (!ok) break;
       }
-      if (wg == 0) {
-        const long long bg = (long long)u.b * a.h_kv + u.g;
-        if (a.parts > 1) {
-          a.part[((long long)u.part * a.B * a.h_kv + bg) * ((long long)a.nkt * kBK) + key] = sum;
-        } else if (key < a.T_max) {
-          float* dst = a.w + bg * a.T_max + key;
-          const bool in = u.valid && key < u.kv;
-          if (!a.accumulate) *dst = in ? sum : 0.f;
-          else if (in && u.n() > 0) *dst += sum;
-        }
-      }
+      if (u.n() > 0) ++nu;
+      if (!writes) continue;
+      if (a.parts > 1) a.part[((long long)u.part * a.B * a.h_kv + bg) * a.part_keys + key] = sum;
+      else if (!a.accumulate && key < a.T_max) *dst = in ? sum : 0.f;
+      else if (a.accumulate && in && u.n() > 0) *dst = old + sum;
     }
   }
   tc::fence_before_sync();
@@ -447,6 +517,234 @@ __global__ void __launch_bounds__(Cfg<D, kNQ>::kThreads, 1)
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// =============================================================================================
+// up to 32 query rows per group: K streams through, m16n8k16 MMAs
+// =============================================================================================
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int MT>
+struct SCfg {
+  static constexpr int kNch = D / 64;
+  static constexpr int kStages = D == 64 ? 8 : MT == 1 ? 6 : 5;
+  static constexpr int kRows = 16 * MT;  // query rows of the tile
+  static constexpr int kWarps = 8;       // consumers
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kKChunk = kBK * 128, kKBytes = kNch * kKChunk;
+  static constexpr int kQChunk = kRows * 128, kQBytes = kNch * kQChunk;
+  static constexpr int kStage = kKBytes + kQBytes;
+  static constexpr int kOffStat = kStages * kStage;              // per stage: -lse2 and position of the rows
+  static constexpr int kOffSeq = kOffStat + kStages * kRows * 8;
+  static constexpr int kOffBar = kOffSeq + kSeqTable * 8;
+  static constexpr int kSmem = kOffBar + 256 + 1024;
+  static_assert(kSmem <= 227 * 1024 && 2 * kStages * 8 + 8 <= 256, "shared memory budget");
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(SCfg<D, MT>::kThreads, 1)
+    kv_weights_small_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
+                            const __grid_constant__ WArgs a) {
+  using C = SCfg<D, MT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // full (stages), empty (stages)
+  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * C::kStages);
+  int2* seq = reinterpret_cast<int2*>(smem + C::kOffSeq);
+  const uint32_t base = smem_u32(smem);
+  auto full = [&](int st) { return smem_u32(&bars[st]); };
+  auto empty = [&](int st) { return smem_u32(&bars[C::kStages + st]); };
+  auto nl2 = [&](int st) { return reinterpret_cast<float*>(smem + C::kOffStat) + st * 2 * C::kRows; };
+  auto cpos = [&](int st) { return reinterpret_cast<int*>(nl2(st) + C::kRows); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(full(i), 1 + 32);  // copies; the producer lanes' statistics
+      mbar_init(empty(i), C::kWarps);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  for (int b = threadIdx.x; b < min(a.B, kSeqTable); b += C::kThreads) seq[b] = sequence(a, b);
+  cta_sync();
+  const int R = a.r * a.S_q;  // query rows of a group
+
+  if (warp == C::kWarps) {
+    // ------------------------------ producer ------------------------------------------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmk);
+      tma_prefetch_desc(&tmq);
+    }
+    // lane = query row of the group: its head and row, and its lse, loaded one unit ahead
+    const int h = lane / a.S_q, i = lane - h * a.S_q;
+    auto lse_of = [&](const Unit& u) {
+      return lane < R ? __ldg(a.lse + ((long long)u.b * a.h_q + u.g * a.r + h) * a.S_q + i) : -INFINITY;
+    };
+    int n = 0, ok = 1;
+    int it = 0;
+    // the next unit with keys to read (n_units: none)
+    auto next = [&](Unit& u) {
+      for (;; ++it) {
+        const long long idx = unit_of(it);
+        if (idx >= a.n_units) return false;
+        u = make_unit<kBK, true>(a, seq, (int)idx);
+        if (!u.valid && u.k0 == 0 && u.g == 0 && lane == 0)
+          set_device_error(a.err, u.kv < 1 || u.kv > a.T_max ? GQA_DEVERR_KV_LEN : GQA_DEVERR_POSITION);
+        if (u.n() > 0) {
+          ++it;
+          return true;
+        }
+      }
+    };
+    Unit u, v;
+    bool have = next(u);
+    float l = have ? lse_of(u) : 0.f;
+    while (have && ok) {
+      const bool more = next(v);
+      const float l_next = more ? lse_of(v) : 0.f;
+      const int st = n % C::kStages, f = n / C::kStages;
+      const int n_sub = (min(kBK, u.kv - u.k0) + a.sub - 1) / a.sub;
+      int row = 0;
+      if (a.block_table) {
+        if (lane < n_sub) {
+          const int key = u.k0 + lane * a.sub;
+          int page = __ldg(a.block_table + (long long)u.b * a.max_pages + key / a.page_size);
+          if (page < 0 || page >= a.num_pages) {
+            set_device_error(a.err, GQA_DEVERR_PAGE);
+            page = 0;
+          }
+          row = (page * a.h_kv + u.g) * a.page_size + key % a.page_size;
+        }
+      } else {
+        row = (u.b * a.h_kv + u.g) * a.T_max + u.k0;
+      }
+      if (lane == 0) {
+        if (f > 0) ok = wait_bar(empty(st), (uint32_t)((f - 1) & 1), abort, a.err);
+        if (ok) {
+          mbar_arrive_expect_tx(full(st), (uint32_t)(n_sub * a.sub * 128 * C::kNch + C::kQBytes));
+          for (int ch = 0; ch < C::kNch; ++ch)
+            tma_load_2d(base + st * C::kStage + C::kKBytes + ch * C::kQChunk, &tmq, full(st), ch * 64,
+                        (u.b * a.h_q + u.g * a.r) * a.S_q);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (lane < n_sub) {
+#pragma unroll
+        for (int ch = 0; ch < C::kNch; ++ch)
+          tma_load_2d(base + st * C::kStage + ch * C::kKChunk + lane * a.sub * 128, &tmk, full(st), ch * 64, row);
+      }
+      if (lane < C::kRows) {
+        // a row without a finite lse (no visible key, padding) takes part in nothing
+        const bool in = l != -INFINITY && l == l;
+        nl2(st)[lane] = in ? -l * kLog2e : 0.f;
+        cpos(st)[lane] = !in ? -1 : a.causal ? (int)min((long long)u.qs + i, (long long)kFar) : kFar;
+      }
+      mbar_arrive(full(st));
+      ++n;
+      u = v;
+      l = l_next;
+      have = more;
+    }
+    if (lane == 0) {  // drain (bounded): no copy may still land in shared memory at exit
+      volatile int no_abort = 0;
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s)
+        if (n > s) wait_bar(full(s), (uint32_t)(((n - 1 - s) / C::kStages) & 1), &no_abort, a.err);
+    }
+    return;
+  }
+
+  // ------------------------------ consumers: 16 keys of each tile per warp -------------------
+  const int gid = lane >> 2, tq = lane & 3;
+  const int reach = a.window > 0 ? a.window : 0x7fffffff;
+  int n = 0;
+  for (int it = 0;; ++it) {
+    const long long idx = unit_of(it);
+    if (idx >= a.n_units) break;
+    const Unit u = make_unit<kBK, true>(a, seq, (int)idx);
+    // lane gid = 2 j + e (below 4) of each quad column tq ends up with key 8 j + 2 tq + e of the warp's 16
+    const int kq = u.k0 + warp * 16 + 2 * tq;  // keys kq, kq + 1, kq + 8, kq + 9
+    const int key = kq + 8 * (gid >> 1) + (gid & 1);
+    const bool writer = gid < 4 && key < a.T_max;
+    const bool in = u.valid && key < u.kv;
+    float* const dst = a.w + ((long long)u.b * a.h_kv + u.g) * a.T_max + key;
+    if (u.n() == 0) {
+      if (writer && !a.accumulate) *dst = 0.f;
+      continue;
+    }
+    // the entry to be added to is loaded ahead of the sum
+    const float old = writer && in && a.accumulate ? *dst : 0.f;
+    const int st = n % C::kStages;
+    // ldmatrix / mma.sync below need the whole warp: leave together if the wait ran out
+    if (!__all_sync(0xffffffffu, wait_bar(full(st), (uint32_t)((n / C::kStages) & 1), abort, a.err))) return;
+    const uint32_t kb = base + st * C::kStage, qb = kb + C::kKBytes;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};  // over this lane's rows, of keys kq, kq + 1, kq + 8, kq + 9
+    if (u.k0 + warp * 16 < u.kv) {
+      float sc[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sc[m][j][0] = sc[m][j][1] = sc[m][j][2] = sc[m][j][3] = 0.f;
+      const int krow = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+      const int qi = lane >> 3;
+      const int qrow = (qi & 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int d8k = ks * 2 + ((lane >> 3) & 1), d8q = ks * 2 + (qi >> 1);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(swz128(kb + (d8k >> 3) * C::kKChunk, krow, d8k & 7), b0, b1, b2, b3);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t qf[4];
+          ldsm_x4(swz128(qb + (d8q >> 3) * C::kQChunk, m * 16 + qrow, d8q & 7), qf[0], qf[1], qf[2], qf[3]);
+          mma_bf16(sc[m][0], qf, b0, b1);
+          mma_bf16(sc[m][1], qf, b2, b3);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = m * 16 + half * 8 + gid;
+          const float nl = nl2(st)[row];
+          const int at = cpos(st)[row];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = kq + 8 * (e >> 1) + (e & 1);
+            // key <= position, and within the window: position - key < window
+            const bool vis = k <= at && at - k < reach;
+            sum[e] += vis ? fast_exp2(fmaf(sc[m][e >> 1][2 * half + (e & 1)], a.sl2, nl)) : 0.f;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty(st));
+    ++n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 4);
+      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 8);
+      sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 16);
+    }
+    const float total = gid == 0 ? sum[0] : gid == 1 ? sum[1] : gid == 2 ? sum[2] : sum[3];
+    if (!writer) continue;
+    if (!a.accumulate) *dst = in ? total : 0.f;
+    else if (in) *dst = old + total;
   }
 }
 
@@ -465,8 +763,8 @@ __global__ void __launch_bounds__(256) kv_weights_join_kernel(const __grid_const
     if (!a.accumulate) *dst = 0.f;
     return;
   }
-  const long long stride = (long long)a.B * a.h_kv * a.nkt * kBK;
-  const float* src = a.part + bg * a.nkt * kBK + key;
+  const long long stride = (long long)a.B * a.h_kv * a.part_keys;
+  const float* src = a.part + bg * a.part_keys + key;
   float sum = 0.f;
   for (int p = 0; p < a.parts; ++p) sum += __ldcg(src + p * stride);
   *dst = a.accumulate ? *dst + sum : sum;
@@ -553,25 +851,26 @@ __global__ void __launch_bounds__(128) kv_weights_fp32_kernel(WArgs a, const flo
 // -------------------------------------------------------------------------------------------------
 // host side
 // -------------------------------------------------------------------------------------------------
-// Tile geometry: P positions (the power of two at or above S_q, at most the tile) of H heads.
+// Tile geometry: P = min(S_q, 128) positions of as many heads as fit (small: all rows of the group).
 struct Geometry {
   bool small;
+  int keys;  // of a unit
   int P, H, N, hblocks, npb, parts;
 };
 Geometry geometry(int B, int h_q, int h_kv, int S_q, int T_max, int num_sms) {
   Geometry m;
   const int r = h_q / h_kv;
-  int p2 = 1;
-  while (p2 < S_q && p2 < 128) p2 <<= 1;
   // every row of the group fits 32 columns: one small Q tile per unit, and more K tiles in flight
-  m.small = S_q <= 32 && (long long)p2 * r <= 32;
-  m.N = m.small ? (p2 * r <= 16 ? 16 : 32) : 128;
-  m.P = p2;
-  m.H = m.N / m.P;
+  m.small = (long long)S_q * r <= 32;
+  m.P = S_q < 128 ? S_q : 128;
+  m.H = m.small ? r : 128 / m.P;
+  m.H = (r + (r + m.H - 1) / m.H - 1) / ((r + m.H - 1) / m.H);  // the same number in every block
+  m.keys = m.small ? kBK : Cfg<64>::kKeys;
+  m.N = (m.P * m.H + 15) / 16 * 16;
   m.hblocks = (r + m.H - 1) / m.H;
   m.npb = (S_q + m.P - 1) / m.P;
   m.parts = 1;
-  const long long units = (long long)B * h_kv * ((T_max + kBK - 1) / kBK);
+  const long long units = (long long)B * h_kv * ((T_max + m.keys - 1) / m.keys);
   const long long tiles = (long long)m.hblocks * m.npb;
   const long long want = ((long long)kUnitsPerSm * num_sms + units - 1) / units;
   const long long most = (tiles + kTilesPerPart - 1) / kTilesPerPart;
@@ -580,25 +879,33 @@ Geometry geometry(int B, int h_q, int h_kv, int S_q, int T_max, int num_sms) {
   return m;
 }
 
-template <int D, int kNQ>
-cudaError_t launch_typed(const WArgs& w, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
-  using C = Cfg<D, kNQ>;
-  auto kern = kv_weights_kernel<D, kNQ>;
-  static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
+template <typename Kernel>
+cudaError_t launch_kernel(Kernel kern, int threads, int smem, bool (&attr_set)[64], const WArgs& w,
+                          const CUtensorMap* tm, int num_sms, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {  // per device: the shared-memory opt-in is set once
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const unsigned grid = (unsigned)(w.n_units < num_sms ? w.n_units : num_sms);
-  kern<<<grid, C::kThreads, C::kSmem, s>>>(tm[0], tm[1], w);
+  kern<<<w.n_units < num_sms ? w.n_units : num_sms, threads, smem, s>>>(tm[0], tm[1], w);
   e = cudaGetLastError();
   if (e != cudaSuccess || w.parts == 1) return e;
   kv_weights_join_kernel<<<dim3((w.T_max + 255) / 256, w.B * w.h_kv), 256, 0, s>>>(w);
   return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_tiles(const WArgs& w, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
+  static bool attr_set[64] = {false};
+  return launch_kernel(kv_weights_kernel<D>, Cfg<D>::kThreads, Cfg<D>::kSmem, attr_set, w, tm, num_sms, s);
+}
+template <int D, int MT>
+cudaError_t launch_small(const WArgs& w, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
+  static bool attr_set[64] = {false};
+  using C = SCfg<D, MT>;
+  return launch_kernel(kv_weights_small_kernel<D, MT>, C::kThreads, C::kSmem, attr_set, w, tm, num_sms, s);
 }
 
 WArgs make_args(const KvWeightsArgs& a, const Geometry& m) {
@@ -618,9 +925,15 @@ WArgs make_args(const KvWeightsArgs& a, const Geometry& m) {
   w.hblocks = m.hblocks;
   w.npb = m.npb;
   w.N = m.N;
-  w.nkt = (a.T_max + kBK - 1) / kBK;
+  w.nkt = (a.T_max + m.keys - 1) / m.keys;
+  w.part_keys = w.nkt * m.keys;
   w.parts = m.parts;
-  w.n_units = (long long)a.B * a.h_kv * w.nkt * m.parts;
+  w.n_units = (int)((long long)a.B * a.h_kv * w.nkt * m.parts);
+  w.div_bg = FastDiv::make((uint32_t)(a.B * a.h_kv));
+  w.div_nkt = FastDiv::make((uint32_t)w.nkt);
+  w.div_parts = FastDiv::make((uint32_t)m.parts);
+  w.div_hkv = FastDiv::make((uint32_t)a.h_kv);
+  w.div_P = FastDiv::make((uint32_t)m.P);
   w.sl2 = a.scale * kLog2e;
   w.causal = a.causal;
   w.window = a.window;
@@ -639,24 +952,33 @@ WArgs make_args(const KvWeightsArgs& a, const Geometry& m) {
 
 int kv_weights_sub(bool paged, int page_size) { return !paged ? 128 : page_size % 64 == 0 ? 64 : 16; }
 
-void kv_weights_tile(int h_q, int h_kv, int S_q, int* P, int* H) {
+KvWeightsTile kv_weights_tile(int h_q, int h_kv, int S_q) {
   const kw::Geometry m = kw::geometry(1, h_q, h_kv, S_q, 1, 0);
-  *P = m.P;
-  *H = m.H;
+  return {m.small, m.P, m.H, S_q * (h_q / h_kv) > 16 ? 32 : 16};
 }
 
 size_t kv_weights_workspace_bytes(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype, int num_sms) {
   if (dtype == GQA_FP32) return 0;
   const kw::Geometry m = kw::geometry(B, h_q, h_kv, S_q, T_max, num_sms);
   if (m.parts == 1) return 0;
-  return (size_t)m.parts * B * h_kv * ((T_max + kw::kBK - 1) / kw::kBK) * kw::kBK * sizeof(float);
+  return (size_t)m.parts * B * h_kv * ((T_max + m.keys - 1) / m.keys) * m.keys * sizeof(float);
 }
 
 cudaError_t launch_kv_weights_bf16(const KvWeightsArgs& a, const CUtensorMap* tmaps, int num_sms, cudaStream_t s) {
   const kw::Geometry m = kw::geometry(a.B, a.h_q, a.h_kv, a.S_q, a.T_max, num_sms);
   const kw::WArgs w = kw::make_args(a, m);
-  if (a.d_h == 128) return m.small ? kw::launch_typed<128, 32>(w, tmaps, num_sms, s) : kw::launch_typed<128, 128>(w, tmaps, num_sms, s);
-  if (a.d_h == 64) return m.small ? kw::launch_typed<64, 32>(w, tmaps, num_sms, s) : kw::launch_typed<64, 128>(w, tmaps, num_sms, s);
+  // units and a unit's tile list times the parts are counted in 32 bits
+  if ((long long)a.B * a.h_kv * w.nkt * m.parts >= (1ll << 31) || (long long)m.npb * m.hblocks * m.parts >= (1ll << 31))
+    return cudaErrorInvalidConfiguration;
+  const bool two = a.S_q * w.r > 16;  // m-tiles of the small kernel
+  if (a.d_h == 128) {
+    if (!m.small) return kw::launch_tiles<128>(w, tmaps, num_sms, s);
+    return two ? kw::launch_small<128, 2>(w, tmaps, num_sms, s) : kw::launch_small<128, 1>(w, tmaps, num_sms, s);
+  }
+  if (a.d_h == 64) {
+    if (!m.small) return kw::launch_tiles<64>(w, tmaps, num_sms, s);
+    return two ? kw::launch_small<64, 2>(w, tmaps, num_sms, s) : kw::launch_small<64, 1>(w, tmaps, num_sms, s);
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -665,7 +987,7 @@ cudaError_t launch_kv_weights_fp32(const KvWeightsArgs& a, cudaStream_t s) {
   const kw::WArgs w = kw::make_args(a, m);
   const long long bg = (long long)a.B * a.h_kv;
   if (bg > 65535) return cudaErrorInvalidConfiguration;
-  kw::kv_weights_fp32_kernel<<<dim3(w.nkt, (unsigned)bg), 128, 0, s>>>(
+  kw::kv_weights_fp32_kernel<<<dim3((a.T_max + kw::kBK - 1) / kw::kBK, (unsigned)bg), 128, 0, s>>>(
       w, reinterpret_cast<const float*>(a.q), reinterpret_cast<const float*>(a.k), a.d_h, a.scale);
   return cudaGetLastError();
 }
