@@ -406,6 +406,45 @@ gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float*
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * kv_evict, kv_evict_paged - shorten every (sequence, KV head)'s cached rows to at most `budget`, by
+ * weight (gqa_kv_weights). With n = kv_len[b] and weights w = weights[b, g, :]:
+ *   n <= budget: all rows stay;
+ *   else the rows [0, sink) and [n - recent, n) stay, and of the rows between them the
+ *   budget - sink - recent with the largest w (ties: the lower row; NaN ranks below every number).
+ * The rows that stay move to rows 0, 1, ... in their order, K, V and weights alike. Keys keep the
+ * rotation they were cached with; appended tokens go to row new_len[b] on, with their own positions
+ * (kv_rope_append's `positions`).
+ *
+ *   k_cache, v_cache (B, h_kv, T_max, d_h); k_out, v_out (B, h_kv, T_out, d_h): the same memory
+ *              (in place, T_out = T_max) or other, not overlapping memory. Rows past the new length
+ *              are left as they were.
+ *   paged      pools and block table as in kv_append_paged; block_table_out NULL: in place; else a
+ *              device int32 (B, max_pages_out) table of the pages written, T_out = max_pages_out *
+ *              page_size: other pages, or the same ones (its first columns). No page of a sequence
+ *              may be written that another sequence of the call reads or writes, and a table names a page once. Rows of
+ *              pages outside the pool are not moved (GQA_DEVERR_PAGE). page_size >= 1.
+ *   weights    (B, h_kv, T_max) fp32; weights_out (B, h_kv, T_out): the same memory or not
+ *              overlapping; written in full, zero from the new length on.
+ *   kept       device int32 (B, h_kv, budget), written: the row each kept row came from, ascending;
+ *              -1 past the new length.
+ *   new_len    device int32[B], written: min(n, budget). It must not overlap kv_len.
+ *   kv_len     device int32[B] or NULL (= T_max); 0 <= kv_len[b] <= T_max, else the sequence is left
+ *              alone, its new_len is kv_len[b] and GQA_DEVERR_KV_LEN is set.
+ *   budget     1 .. T_out; sink, recent >= 0, sink + recent <= budget.
+ * Any d_h >= 1. B * h_kv <= 65535. Two launches in order on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+gqa_status kv_evict(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
+                    const float* weights, float* weights_out, int32_t* kept, int32_t* new_len,
+                    const int32_t* kv_len, int B, int h_kv, int T_max, int T_out, int budget, int sink,
+                    int recent, int d_h, gqa_dtype dtype, void* stream);
+gqa_status kv_evict_paged(void* k_pages, void* v_pages, const int32_t* block_table,
+                          const int32_t* block_table_out, const float* weights, float* weights_out,
+                          int32_t* kept, int32_t* new_len, const int32_t* kv_len, int B, int h_kv,
+                          int num_pages, int page_size, int max_pages, int max_pages_out, int budget,
+                          int sink, int recent, int d_h, gqa_dtype dtype, void* stream);
+
+/*
  * gqa_get_device_error - synchronise `stream`, then read and clear the sticky device error word
  * of the current device. *code receives a GQA_DEVERR_* value. Returns GQA_ERR_DEVICE when the word
  * was non-zero, GQA_OK when it was zero, GQA_ERR_CUDA if the read failed.

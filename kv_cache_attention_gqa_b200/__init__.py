@@ -18,6 +18,8 @@ from ._lib import (  # noqa: F401
     get_device_error,
     kv_append,
     kv_append_paged,
+    kv_evict,
+    kv_evict_paged,
     kv_rope_append,
     kv_rope_append_paged,
     kv_weights,

@@ -58,6 +58,8 @@ SIGNATURES = {
     "gqa_kv_weights": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _I, _P, _Z, _P]),
     "gqa_kv_weights_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _I,
                                   _P, _Z, _P]),
+    "kv_evict": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "kv_evict_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "gqa_get_device_error": (_I, [ctypes.POINTER(_I), _P]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
     "gqa_version": (ctypes.c_char_p, []),
@@ -674,3 +676,76 @@ def kv_weights_paged(q: torch.Tensor, k_pages: torch.Tensor, block_table, lse: t
         _ptr(q), _ptr(k_pages), _ptr(lse), _ptr(weights), _ptr(qs), _ptr(kl), _ptr(bt), B, h_q, h_kv, S, num_pages,
         page_size, max_pages, d, _scale(scale), 1 if causal else 0, int(window), acc, dt, _ptr(ws), nws, _stream()))
     return weights
+
+
+def _evict_args(k, v, weights, B, h_kv, T_max, T_out, budget, kv_len, weights_out, kept):
+    """Checks and arguments shared by kv_evict and kv_evict_paged."""
+    _need_cuda(k, v, weights, weights_out, kept)
+    dt = _dtype_code(k)
+    if v.dtype != k.dtype:
+        raise TypeError("the caches must share one dtype")
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (B, h_kv, T_max):
+        raise ValueError(f"weights must be float32 of shape {(B, h_kv, T_max)}")
+    budget = int(budget)
+    if budget < 1 or budget > T_out:
+        raise ValueError(f"budget must be between 1 and {T_out}")
+    if weights_out is None:
+        if T_out != T_max:
+            raise ValueError("weights_out must be given when the caches are not shortened in place")
+        weights_out = weights
+    _out(weights_out, (B, h_kv, T_out), torch.float32, weights.device)
+    kept = _out(kept, (B, h_kv, budget), torch.int32, weights.device)
+    new_len = torch.empty(B, dtype=torch.int32, device=weights.device)
+    return dt, budget, weights_out, kept, new_len, _int_vec(kv_len, B, weights.device, "kv_len")
+
+
+def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor, budget: int, *, kv_len=None,
+             sink: int = 0, recent: int = 0, k_out=None, v_out=None, weights_out=None, kept=None):
+    """Shorten every KV head's rows to at most ``budget``: the first ``sink``, the last ``recent`` and the
+    heaviest of the others (``weights`` from ``kv_weights``; ties to the lower row) move to the front in
+    their order. In place, or into ``k_out``, ``v_out``, ``weights_out`` of (B, h_kv, T_out, d_h) and
+    (B, h_kv, T_out). Weights past the new length become zero. Returns (kept, new_len): the rows kept
+    (B, h_kv, budget) int32, -1 past the new length, and the new lengths (B,) int32."""
+    _need_cuda(k_cache, v_cache, k_out, v_out)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache must both be (B, h_kv, T_max, d_h)")
+    B, h_kv, T_max, d = k_cache.shape
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out must be given together")
+    T_out = T_max
+    if k_out is None:
+        k_out, v_out = k_cache, v_cache
+    else:
+        if k_out.dim() != 4 or v_out.shape != k_out.shape or tuple(k_out.shape) != (B, h_kv, k_out.shape[2], d):
+            raise ValueError("k_out / v_out must both be (B, h_kv, T_out, d_h)")
+        if k_out.dtype != k_cache.dtype or v_out.dtype != k_cache.dtype:
+            raise TypeError("the caches must share one dtype")
+        if weights_out is None:
+            raise ValueError("weights_out must be given with k_out and v_out")
+        T_out = k_out.shape[2]
+    dt, budget, weights_out, kept, new_len, kl = _evict_args(k_cache, v_cache, weights, B, h_kv, T_max, T_out,
+                                                             budget, kv_len, weights_out, kept)
+    _check("kv_evict", _lib.kv_evict(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_out), _ptr(v_out), _ptr(weights), _ptr(weights_out), _ptr(kept),
+        _ptr(new_len), _ptr(kl), B, h_kv, T_max, T_out, budget, int(sink), int(recent), d, dt, _stream()))
+    return kept, new_len
+
+
+def kv_evict_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table, weights: torch.Tensor, budget: int,
+                   *, kv_len=None, sink: int = 0, recent: int = 0, block_table_out=None, weights_out=None,
+                   kept=None):
+    """``kv_evict`` over a paged cache: in place, or with ``block_table_out`` (B, max_pages_out) into other pages
+    of the same pools (or the first ones of each sequence)."""
+    num_pages, h_kv, page_size, d = _pool_shape(k_pages, v_pages)
+    _need_cuda(k_pages, v_pages)
+    B = weights.shape[0]
+    bt = _block_table(block_table, B, k_pages.device)
+    bo = None if block_table_out is None else _block_table(block_table_out, B, k_pages.device)
+    max_out = bt.shape[1] if bo is None else bo.shape[1]
+    dt, budget, weights_out, kept, new_len, kl = _evict_args(k_pages, v_pages, weights, B, h_kv, bt.shape[1] * page_size,
+                                                             max_out * page_size, budget, kv_len, weights_out, kept)
+    _check("kv_evict_paged", _lib.kv_evict_paged(
+        _ptr(k_pages), _ptr(v_pages), _ptr(bt), _ptr(bo), _ptr(weights), _ptr(weights_out), _ptr(kept), _ptr(new_len),
+        _ptr(kl), B, h_kv, num_pages, page_size, bt.shape[1], max_out, budget, int(sink), int(recent), d, dt,
+        _stream()))
+    return kept, new_len

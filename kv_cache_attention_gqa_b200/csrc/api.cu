@@ -322,6 +322,31 @@ gqa_status kv_weights_impl(KvWeightsArgs a, gqa_dtype dtype, size_t workspace_by
   if (!ok) return GQA_ERR_CUDA;
   return from_cuda(launch_kv_weights_bf16(a, maps, sms, s));
 }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Checks shared by kv_evict and kv_evict_paged, and the launch.
+gqa_status evict_impl(EvictArgs& a, int d_h, gqa_dtype dtype, void* stream) {
+  if (!a.k || !a.v || !a.k_out || !a.v_out || !a.w || !a.w_out || !a.kept || !a.new_len) return GQA_ERR_INVALID_ARG;
+  if (a.B <= 0 || a.h_kv <= 0 || a.T_max <= 0 || a.T_out <= 0 || d_h <= 0) return GQA_ERR_INVALID_ARG;
+  if (a.budget <= 0 || a.sink < 0 || a.recent < 0 || (long long)a.sink + a.recent > a.budget) return GQA_ERR_INVALID_ARG;
+  if (a.budget > a.T_out) return GQA_ERR_INVALID_ARG;
+  if (dtype != GQA_BF16 && dtype != GQA_FP32) return GQA_ERR_INVALID_ARG;
+  // every block reads kv_len after new_len may be written
+  if (a.kv_len && overlap(a.kv_len, (size_t)a.B * 4, a.new_len, (size_t)a.B * 4)) return GQA_ERR_INVALID_ARG;
+  const size_t bg = (size_t)a.B * a.h_kv;
+  if (a.w_out == a.w ? a.T_out != a.T_max
+                     : overlap(a.w, bg * a.T_max * 4, a.w_out, bg * a.T_out * 4))
+    return GQA_ERR_INVALID_ARG;
+  if ((long long)bg > 65535) return GQA_ERR_UNSUPPORTED;
+  a.err = device_error_ptr();
+  const int sms = sm_count();
+  if (!a.err || sms <= 0) return GQA_ERR_CUDA;
+  return from_cuda(launch_kv_evict(a, d_h, dtype == GQA_BF16 ? 2 : 4, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
 }  // namespace
 
 extern "C" {
@@ -783,6 +808,77 @@ gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float*
   a.page_size = page_size;
   a.num_pages = num_pages;
   return kv_weights_impl(a, dtype, workspace_bytes, stream);
+}
+
+gqa_status kv_evict(const void* k_cache, const void* v_cache, void* k_out, void* v_out,
+                    const float* weights, float* weights_out, int32_t* kept, int32_t* new_len,
+                    const int32_t* kv_len, int B, int h_kv, int T_max, int T_out, int budget, int sink,
+                    int recent, int d_h, gqa_dtype dtype, void* stream) {
+  EvictArgs a;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.w = weights;
+  a.w_out = weights_out;
+  a.kept = kept;
+  a.new_len = new_len;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.h_kv = h_kv;
+  a.T_max = T_max;
+  a.T_out = T_out;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.in_place = k_cache == k_out ? 1 : 0;
+  if (B > 0 && h_kv > 0 && T_max > 0 && T_out > 0 && d_h > 0) {
+    // in place both caches are, over the same rows; else no output overlaps an input or the other output
+    const size_t row = (size_t)d_h * (dtype == GQA_BF16 ? 2 : 4);
+    const size_t in = (size_t)B * h_kv * T_max * row, out = (size_t)B * h_kv * T_out * row;
+    if (a.in_place ? v_cache != v_out || T_out != T_max
+                   : overlap(k_cache, in, k_out, out) || overlap(v_cache, in, v_out, out))
+      return GQA_ERR_INVALID_ARG;
+    if (overlap(k_cache, in, v_out, out) || overlap(v_cache, in, k_out, out) || overlap(k_out, out, v_out, out))
+      return GQA_ERR_INVALID_ARG;
+  }
+  return evict_impl(a, d_h, dtype, stream);
+}
+
+gqa_status kv_evict_paged(void* k_pages, void* v_pages, const int32_t* block_table,
+                          const int32_t* block_table_out, const float* weights, float* weights_out,
+                          int32_t* kept, int32_t* new_len, const int32_t* kv_len, int B, int h_kv,
+                          int num_pages, int page_size, int max_pages, int max_pages_out, int budget,
+                          int sink, int recent, int d_h, gqa_dtype dtype, void* stream) {
+  if (!block_table || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
+  if (!block_table_out) max_pages_out = max_pages;
+  if (max_pages_out <= 0) return GQA_ERR_INVALID_ARG;
+  const long long T_max = (long long)max_pages * page_size, T_out = (long long)max_pages_out * page_size;
+  if (T_max >= (1ll << 31) || T_out >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  if (k_pages == v_pages) return GQA_ERR_INVALID_ARG;
+  EvictArgs a;
+  a.k = a.k_out = k_pages;
+  a.v = a.v_out = v_pages;
+  a.w = weights;
+  a.w_out = weights_out;
+  a.kept = kept;
+  a.new_len = new_len;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.h_kv = h_kv;
+  a.T_max = (int)T_max;
+  a.T_out = (int)T_out;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.in_place = block_table_out ? 0 : 1;
+  a.block_table = block_table;
+  a.block_table_out = block_table_out ? block_table_out : block_table;
+  a.max_pages = max_pages;
+  a.max_pages_out = max_pages_out;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  return evict_impl(a, d_h, dtype, stream);
 }
 
 }  // extern "C"

@@ -83,6 +83,27 @@ size_t kv_weights_workspace_bytes(int B, int h_q, int h_kv, int S_q, int T_max, 
 cudaError_t launch_kv_weights_bf16(const KvWeightsArgs& a, const CUtensorMap* tmaps, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_weights_fp32(const KvWeightsArgs& a, cudaStream_t s);
 
+// Eviction from the cache (kv_evict.cu).
+struct EvictArgs {
+  const void* k;
+  const void* v;
+  void* k_out;
+  void* v_out;
+  const float* w;
+  float* w_out;
+  int32_t* kept;     // (B, h_kv, budget)
+  int32_t* new_len;  // (B)
+  const int32_t* kv_len;
+  int B, h_kv, T_max, T_out, budget, sink, recent;
+  int in_place;  // the caches are written where they are read
+  unsigned* err;
+  // paged cache: source and destination tables over one pool
+  const int32_t* block_table = nullptr;
+  const int32_t* block_table_out = nullptr;
+  int max_pages = 0, max_pages_out = 0, page_size = 0, num_pages = 0;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, int d_h, int elem_bytes, int num_sms, cudaStream_t s);
+
 struct PrefillArgs {
   const void* q;
   const void* k;

@@ -1,0 +1,298 @@
+// Eviction from the KV cache by accumulated attention weight: of each (sequence, KV head)'s n cached keys
+// the first `sink`, the last `recent` and the budget - sink - recent heaviest of the others are kept and
+// moved to the front, in their order, in the caller's cache (in place) or into another.
+//
+// Two launches.
+//   select  one CTA per (sequence, KV head). The threshold weight is found by a radix selection over the
+//           weights' bits mapped to unsigned integers of the same order: passes of 11, 11 and 10 bits, each a
+//           histogram in shared memory and a scan of its counts (with 8 bits the first pass would be the
+//           exponent alone, a handful of bins that every thread of a warp adds to in turn); the weights are
+//           read from DRAM once and kept in shared memory while they fit. Then one pass over the keys in
+//           order writes the kept indices: everything above the threshold, and of the keys equal to it the
+//           first ones. Bound by latency: a few thousand keys per block, a dozen dependent phases.
+//   move    rows of K, V and the weights, bound by DRAM (kept rows once in, once out). Kept indices ascend, so
+//           a row's source is at or behind its destination (kept[i] >= i): moving in order, batch by batch,
+//           with every load of a batch before its first store, never overwrites a row still to be read, also
+//           in place. Columns are independent, so a (sequence, head, tensor) is cut into column slices,
+//           one CTA each, which need no order among them; a copy into another contiguous cache is cut along
+//           the rows too. The next batch's loads are issued before the current batch's stores (its sources lie
+//           behind the current destinations).
+
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gqa {
+namespace ev {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeep = 48 * 1024;  // weights kept in shared memory (192 KiB)
+constexpr int kBins = 2048;  // 11 bits a pass: two bins a thread
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 4;  // vectors in flight per thread and batch
+
+// Weights in the order of eviction: unsigned, larger = kept longer; NaN ranks lowest.
+__device__ __forceinline__ uint32_t rank_bits(float w) {
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);  // -0 equals 0
+  if (w != w) return 0u;
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t keep[];  // ranks of the middle keys, when they fit
+  __shared__ int hist[kBins];
+  __shared__ int warp_sum[kSelWarps], warp_gt[kSelWarps], warp_eq[kSelWarps];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  const int g = blockIdx.x % a.h_kv, b = blockIdx.x / a.h_kv;
+  const long long bg = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = a.kv_len ? a.kv_len[b] : a.T_max;
+  const bool valid = n >= 0 && n <= a.T_max;
+  int32_t* kept = a.kept + bg * a.budget;
+  const int len = !valid ? 0 : n < a.budget ? n : a.budget;
+  if (threadIdx.x == 0) {
+    if (!valid && g == 0) set_device_error(a.err, GQA_DEVERR_KV_LEN);
+    if (g == 0) a.new_len[b] = valid ? len : n;
+  }
+  if (!valid || n <= a.budget) {  // everything stays
+    for (int i = threadIdx.x; i < a.budget; i += kSelThreads) kept[i] = i < len ? i : -1;
+    return;
+  }
+  const float* w = a.w + bg * a.T_max;
+  const int lo = a.sink, hi = n - a.recent, m = hi - lo;  // the keys that compete: [lo, hi)
+  const int need = a.budget - a.sink - a.recent;          // of which so many stay (need < m)
+  const bool fits = m <= kSelKeep;
+  auto rank = [&](int i) { return fits ? keep[i] : rank_bits(__ldg(w + lo + i)); };
+  if (fits)
+    for (int i = threadIdx.x; i < m; i += kSelThreads) keep[i] = rank_bits(__ldg(w + lo + i));
+  for (int i = threadIdx.x; i < a.sink; i += kSelThreads) kept[i] = i;
+  for (int i = threadIdx.x; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = hi + i;
+  if (need == 0) return;
+
+  // threshold: the need-th largest rank, 11, 11 and 10 bits at a time
+  uint32_t prefix = 0;
+  int left = need;  // how many of the keys that share the prefix stay
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    const uint32_t mask = (1u << (top - shift)) - 1u;
+    for (int i0 = warp * 32; i0 < m; i0 += kSelThreads) {
+      const int i = i0 + lane;
+      const uint32_t r = i < m ? rank(i) : 0u;
+      const bool in = i < m && (pass == 0 || (r >> top) == (prefix >> top));
+      const uint32_t ins = __ballot_sync(0xffffffffu, in);
+      if (ins == 0) continue;
+      const int bin = (int)(r >> shift & mask);
+      // equal bins across the warp (equal weights, above all zeros) are added once
+      const int first = __shfl_sync(0xffffffffu, bin, __ffs(ins) - 1);
+      if (__all_sync(0xffffffffu, !in || bin == first)) {
+        if (lane == 0) atomicAdd(&hist[first], __popc(ins));
+      } else if (in) {
+        atomicAdd(&hist[bin], 1);
+      }
+    }
+    __syncthreads();
+    // thread t holds bins 2047 - 2t and 2046 - 2t; counts of the bins above them by a scan over the block
+    const int c0 = hist[kBins - 1 - 2 * threadIdx.x], c1 = hist[kBins - 2 - 2 * threadIdx.x];
+    int above = c0 + c1;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, above, off);
+      if (lane >= off) above += t;
+    }
+    if (lane == 31) warp_sum[warp] = above;
+    __syncthreads();
+    above += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0) - c0 - c1;
+    if (above < left && above + c0 + c1 >= left) {  // exactly one thread
+      const bool second = above + c0 < left;
+      s_prefix = prefix | (uint32_t)(kBins - 1 - 2 * (int)threadIdx.x - (second ? 1 : 0)) << shift;
+      s_need = left - above - (second ? c0 : 0);
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_need;
+  }
+
+  // kept indices in order: ranks above the threshold, and the first `left` equal to it. A warp takes a
+  // contiguous range; counts of the warps before it give its places.
+  const int per = ((m + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int i0 = min(m, warp * per), i1 = min(m, i0 + per);
+  int gt = 0, eq = 0;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t r = i + lane < i1 ? rank(i + lane) : 0u;
+    const bool in = i + lane < i1;
+    gt += __popc(__ballot_sync(0xffffffffu, in && r > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, in && r == prefix));
+  }
+  if (lane == 0) {
+    warp_gt[warp] = gt;
+    warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  int gt0 = 0, eq0 = 0;  // before this warp's range
+  for (int k = 0; k < warp; ++k) {
+    gt0 += warp_gt[k];
+    eq0 += warp_eq[k];
+  }
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const uint32_t r = in ? rank(i + lane) : 0u;
+    const uint32_t bg_ = __ballot_sync(0xffffffffu, in && r > prefix);
+    const uint32_t be = __ballot_sync(0xffffffffu, in && r == prefix);
+    const uint32_t below = (1u << lane) - 1u;
+    const int g_at = gt0 + __popc(bg_ & below), e_at = eq0 + __popc(be & below);
+    if (in && (r > prefix || (r == prefix && e_at < left)))
+      kept[a.sink + g_at + min(e_at, left)] = lo + i + lane;
+    gt0 += __popc(bg_);
+    eq0 += __popc(be);
+  }
+}
+
+// Rows kept[i] -> i of one column slice of K or of V, or (the last job) the weights.
+template <typename Vec>
+__global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const __grid_constant__ EvictArgs a, int vecs,
+                                                                     int slice, int n_slices, int row_split) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept indices are written
+  const long long bg = blockIdx.y;
+  const int b = (int)(bg / a.h_kv), g = (int)(bg - (long long)b * a.h_kv);
+  const int n = a.kv_len ? a.kv_len[b] : a.T_max;
+  if (n < 0 || n > a.T_max) return;
+  const int len = n < a.budget ? n : a.budget;
+  const int32_t* kept = a.kept + bg * a.budget;
+  const int job = blockIdx.x;
+  if (job == 2 * n_slices * row_split) {
+    // the weights: one float a row, and zero from the new length on, where appended keys will count from
+    const float* src = a.w + bg * a.T_max;
+    float* dst = a.w_out + bg * a.T_out;
+    const bool stay = a.w_out == a.w && n <= a.budget;
+    for (int base = 0; base < len && !stay; base += kMoveThreads) {
+      const int i = base + threadIdx.x;
+      const float x = i < len ? src[kept[i]] : 0.f;
+      __syncthreads();
+      if (i < len) dst[i] = x;
+    }
+    if (a.w_out == a.w) __syncthreads();
+    for (int i = len + threadIdx.x; i < a.T_out; i += kMoveThreads) dst[i] = 0.f;
+    return;
+  }
+  if (a.in_place && n <= a.budget) return;
+  const int part = job % row_split, sl = (job / row_split) % n_slices, is_v = job / (row_split * n_slices);
+  const Vec* src = reinterpret_cast<const Vec*>(is_v ? a.v : a.k);
+  Vec* dst = reinterpret_cast<Vec*>(is_v ? a.v_out : a.k_out);
+  const int c0 = sl * slice, nc = min(slice, vecs - c0);  // this slice's vectors of a row
+  const int rows = kMoveThreads / slice;                  // rows a block moves at once
+  const int rl = threadIdx.x / slice, c = threadIdx.x - rl * slice;
+  const bool lane_ok = rl < rows && c < nc;
+  // rows [r0, r1) of this block (an in-place move is never cut along the rows)
+  const int per = (len + row_split - 1) / row_split;
+  const int r0 = min(len, part * per), r1 = min(len, r0 + per);
+  auto row_of = [&](const int32_t* table, int max_pages, long long T, int at) -> long long {
+    if (!table) return bg * T + at;
+    int page = table[(long long)b * max_pages + at / a.page_size];
+    if (page < 0 || page >= a.num_pages) {
+      set_device_error(a.err, GQA_DEVERR_PAGE);
+      return -1;
+    }
+    return ((long long)page * a.h_kv + g) * a.page_size + at % a.page_size;
+  };
+  Vec cur[kMoveUnroll], nxt[kMoveUnroll];
+  // vectors of the batch from row r on; < 0 destinations are not written
+  auto load = [&](int r, Vec (&x)[kMoveUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int i = r + u * rows + rl;
+      if (!lane_ok || i >= r1) continue;
+      const long long at = row_of(a.block_table, a.max_pages, a.T_max, kept[i]);
+      if (at >= 0) x[u] = src[at * vecs + c0 + c];
+    }
+  };
+  auto store = [&](int r, const Vec (&x)[kMoveUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int i = r + u * rows + rl;
+      if (!lane_ok || i >= r1) continue;
+      if (a.in_place && kept[i] == i) continue;
+      if (a.block_table && row_of(a.block_table, a.max_pages, a.T_max, kept[i]) < 0) continue;
+      const long long at = row_of(a.block_table_out, a.max_pages_out, a.T_out, i);
+      if (at >= 0) dst[at * vecs + c0 + c] = x[u];
+    }
+  };
+  const int batch = rows * kMoveUnroll;
+  if (r0 < r1) load(r0, cur);
+  for (int r = r0; r < r1; r += batch) {
+    if (r + batch < r1) load(r + batch, nxt);
+    __syncthreads();  // every load of this batch (and the next) comes before its stores
+    store(r, cur);
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) cur[u] = nxt[u];
+  }
+}
+
+template <typename Vec>
+cudaError_t launch_move(const EvictArgs& a, long long row_bytes, int num_sms, cudaStream_t s) {
+  const int vecs = (int)(row_bytes / sizeof(Vec));
+  const long long bg = (long long)a.B * a.h_kv;
+  // column slices: 128 bytes where that gives every SM two blocks, down to 32 (a DRAM sector) where not
+  int slice = 128 / (int)sizeof(Vec);
+  const int least = 32 / (int)sizeof(Vec);
+  auto slices = [&](int w) { return (vecs + w - 1) / w; };
+  while (slice > least && bg * 2 * slices(slice) < 2ll * num_sms) slice /= 2;
+  while (slice > 1 && slice / 2 >= vecs) slice /= 2;
+  const int n_slices = slices(slice);
+  // a copy into another contiguous cache has no order: cut it along the rows until the SMs have work
+  int split = 1;
+  if (!a.in_place && !a.block_table) {
+    const int rows = kMoveThreads / slice * kMoveUnroll;
+    const int most = (a.budget + rows - 1) / rows;
+    const long long want = (16ll * num_sms + bg * 2 * n_slices - 1) / (bg * 2 * n_slices);
+    split = (int)(want < most ? want : most);
+    if (split < 1) split = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * n_slices * split + 1), (unsigned)bg);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_move_kernel<Vec>, a, vecs, slice, n_slices, split);
+  if (e != cudaSuccess) {  // a stream that does not take dependent launches
+    (void)cudaGetLastError();
+    cfg.numAttrs = 0;
+    e = cudaLaunchKernelEx(&cfg, kv_evict_move_kernel<Vec>, a, vecs, slice, n_slices, split);
+  }
+  return e;
+}
+
+}  // namespace ev
+
+cudaError_t launch_kv_evict(const EvictArgs& a, int d_h, int elem_bytes, int num_sms, cudaStream_t s) {
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(ev::kv_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             ev::kSelKeep * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  const int keep = a.T_max < ev::kSelKeep ? a.T_max : ev::kSelKeep;
+  ev::kv_evict_select_kernel<<<(unsigned)(a.B * a.h_kv), ev::kSelThreads, (size_t)keep * 4, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long row_bytes = (long long)d_h * elem_bytes;
+  const uintptr_t all = (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.k_out | (uintptr_t)a.v_out;
+  if (row_bytes % 16 == 0 && all % 16 == 0) return ev::launch_move<uint4>(a, row_bytes, num_sms, s);
+  if (row_bytes % 4 == 0 && all % 4 == 0) return ev::launch_move<uint32_t>(a, row_bytes, num_sms, s);
+  return ev::launch_move<uint16_t>(a, row_bytes, num_sms, s);
+}
+
+}  // namespace gqa

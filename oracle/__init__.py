@@ -33,6 +33,7 @@ from .backward import attention_backward_ref, softmax_backward_rowterm
 from .mla import mla_decode_ref, mla_explicit_ref
 from .rope import rope_ref
 from .kv_weights import kv_weights_ref
+from .kv_evict import kv_evict_ref
 from . import ledgers
 
 __all__ = [
@@ -54,5 +55,6 @@ __all__ = [
     "mla_explicit_ref",
     "rope_ref",
     "kv_weights_ref",
+    "kv_evict_ref",
     "ledgers",
 ]
