@@ -341,7 +341,11 @@ gqa_status evict_impl(EvictArgs& a, int d_h, gqa_dtype dtype, void* stream) {
   if (a.w_out == a.w ? a.T_out != a.T_max
                      : overlap(a.w, bg * a.T_max * 4, a.w_out, bg * a.T_out * 4))
     return GQA_ERR_INVALID_ARG;
-  if ((long long)bg > 65535) return GQA_ERR_UNSUPPORTED;
+  // rows are counted in 32 bits
+  const long long rows = a.block_table ? (long long)a.num_pages * a.h_kv * a.page_size : (long long)bg * a.T_max;
+  if (rows >= (1ll << 31) || (long long)bg * a.T_max >= (1ll << 31) || (long long)bg * a.T_out >= (1ll << 31) ||
+      (long long)bg > 65535)
+    return GQA_ERR_UNSUPPORTED;
   a.err = device_error_ptr();
   const int sms = sm_count();
   if (!a.err || sms <= 0) return GQA_ERR_CUDA;

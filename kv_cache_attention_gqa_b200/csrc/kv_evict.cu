@@ -32,6 +32,7 @@ constexpr int kSelKeep = 48 * 1024;  // weights kept in shared memory (192 KiB)
 constexpr int kBins = 2048;  // 11 bits a pass: two bins a thread
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // vectors in flight per thread and batch
+constexpr int kTable = 1024;    // rows whose addresses are worked out together
 
 // Weights in the order of eviction: unsigned, larger = kept longer; NaN ranks lowest.
 __device__ __forceinline__ uint32_t rank_bits(float w) {
@@ -41,7 +42,8 @@ __device__ __forceinline__ uint32_t rank_bits(float w) {
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint32_t keep[];  // ranks of the middle keys, when they fit
+  extern __shared__ uint4 keep4[];  // ranks of the competing keys, when they fit (a whole number of fours)
+  uint32_t* const keep = reinterpret_cast<uint32_t*>(keep4);
   __shared__ int hist[kBins];
   __shared__ int warp_sum[kSelWarps], warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ uint32_t s_prefix;
@@ -66,8 +68,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
   const int need = a.budget - a.sink - a.recent;          // of which so many stay (need < m)
   const bool fits = m <= kSelKeep;
   auto rank = [&](int i) { return fits ? keep[i] : rank_bits(__ldg(w + lo + i)); };
-  if (fits)
-    for (int i = threadIdx.x; i < m; i += kSelThreads) keep[i] = rank_bits(__ldg(w + lo + i));
+  if (fits) {
+    constexpr int kU = 8;  // loads in flight per thread
+    for (int i0 = threadIdx.x; i0 < m; i0 += kU * kSelThreads) {
+      float x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) x[u] = i0 + u * kSelThreads < m ? __ldg(w + lo + i0 + u * kSelThreads) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i0 + u * kSelThreads < m) keep[i0 + u * kSelThreads] = rank_bits(x[u]);
+    }
+  }
   for (int i = threadIdx.x; i < a.sink; i += kSelThreads) kept[i] = i;
   for (int i = threadIdx.x; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = hi + i;
   if (need == 0) return;
@@ -81,19 +92,28 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
     for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     const uint32_t mask = (1u << (top - shift)) - 1u;
-    for (int i0 = warp * 32; i0 < m; i0 += kSelThreads) {
-      const int i = i0 + lane;
-      const uint32_t r = i < m ? rank(i) : 0u;
-      const bool in = i < m && (pass == 0 || (r >> top) == (prefix >> top));
-      const uint32_t ins = __ballot_sync(0xffffffffu, in);
-      if (ins == 0) continue;
-      const int bin = (int)(r >> shift & mask);
-      // equal bins across the warp (equal weights, above all zeros) are added once
-      const int first = __shfl_sync(0xffffffffu, bin, __ffs(ins) - 1);
-      if (__all_sync(0xffffffffu, !in || bin == first)) {
-        if (lane == 0) atomicAdd(&hist[first], __popc(ins));
-      } else if (in) {
-        atomicAdd(&hist[bin], 1);
+    // four neighbours a thread; where they share a bin (equal weights, above all zeros) they are added at once
+    for (int i = 4 * threadIdx.x; i < m; i += 4 * kSelThreads) {
+      uint32_t r[4];
+      if (fits) {
+        const uint4 q = keep4[i / 4];
+        r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = i + e < m ? rank(i + e) : 0u;
+      }
+      int bin[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = i + e < m && (pass == 0 || (r[e] >> top) == (prefix >> top));
+        bin[e] = in ? (int)(r[e] >> shift & mask) : -1;
+      }
+      if (bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3]) {
+        if (bin[0] >= 0) atomicAdd(&hist[bin[0]], 4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (bin[e] >= 0) atomicAdd(&hist[bin[e]], 1);
       }
     }
     __syncthreads();
@@ -188,46 +208,68 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const __gri
   const int rows = kMoveThreads / slice;                  // rows a block moves at once
   const int rl = threadIdx.x / slice, c = threadIdx.x - rl * slice;
   const bool lane_ok = rl < rows && c < nc;
-  // rows [r0, r1) of this block (an in-place move is never cut along the rows)
+  // rows [r0, r1) of this block (a move that may be in place is never cut along the rows)
   const int per = (len + row_split - 1) / row_split;
   const int r0 = min(len, part * per), r1 = min(len, r0 + per);
-  auto row_of = [&](const int32_t* table, int max_pages, long long T, int at) -> long long {
-    if (!table) return bg * T + at;
-    int page = table[(long long)b * max_pages + at / a.page_size];
+  // Source and destination rows, a table of kTable at a time (dst < 0: not moved). Every thread of a row
+  // working them out for itself, kept index, table entry and divisions, was the longer part of the kernel.
+  __shared__ int s_src[2][kTable], s_dst[2][kTable];
+  auto row_of = [&](const int32_t* table, int max_pages, int T, int at) -> int {
+    if (!table) return (int)(bg * T + at);
+    const int pg = at / a.page_size;
+    const int page = table[(long long)b * max_pages + pg];
     if (page < 0 || page >= a.num_pages) {
       set_device_error(a.err, GQA_DEVERR_PAGE);
       return -1;
     }
-    return ((long long)page * a.h_kv + g) * a.page_size + at % a.page_size;
+    return (page * a.h_kv + g) * a.page_size + at - pg * a.page_size;
   };
+  auto fill = [&](int t) {  // table t: rows r0 + t kTable ...
+    for (int k = threadIdx.x; k < kTable; k += kMoveThreads) {
+      const int i = r0 + t * kTable + k;
+      int from = 0, to = -1;
+      if (i < r1) {
+        const int at = kept[i];
+        if (!a.in_place || at != i) {
+          from = row_of(a.block_table, a.max_pages, a.T_max, at);
+          to = from < 0 ? -1 : row_of(a.block_table_out, a.max_pages_out, a.T_out, i);
+        }
+      }
+      s_src[t & 1][k] = from;
+      s_dst[t & 1][k] = to;
+    }
+  };
+  const int batch = rows * kMoveUnroll;  // divides kTable
+  const int per_table = kTable / batch, n_batches = (r1 - r0 + batch - 1) / batch;
   Vec cur[kMoveUnroll], nxt[kMoveUnroll];
-  // vectors of the batch from row r on; < 0 destinations are not written
-  auto load = [&](int r, Vec (&x)[kMoveUnroll]) {
+  auto load = [&](int n_, Vec (&x)[kMoveUnroll]) {
+    const int t = (n_ / per_table) & 1, k0 = n_ % per_table * batch + rl;
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u)
+      if (lane_ok && s_dst[t][k0 + u * rows] >= 0) x[u] = src[(long long)s_src[t][k0 + u * rows] * vecs + c0 + c];
+  };
+  auto store = [&](int n_, const Vec (&x)[kMoveUnroll]) {
+    const int t = (n_ / per_table) & 1, k0 = n_ % per_table * batch + rl;
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = r + u * rows + rl;
-      if (!lane_ok || i >= r1) continue;
-      const long long at = row_of(a.block_table, a.max_pages, a.T_max, kept[i]);
-      if (at >= 0) x[u] = src[at * vecs + c0 + c];
+      const int to = s_dst[t][k0 + u * rows];
+      if (lane_ok && to >= 0) dst[(long long)to * vecs + c0 + c] = x[u];
     }
   };
-  auto store = [&](int r, const Vec (&x)[kMoveUnroll]) {
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = r + u * rows + rl;
-      if (!lane_ok || i >= r1) continue;
-      if (a.in_place && kept[i] == i) continue;
-      if (a.block_table && row_of(a.block_table, a.max_pages, a.T_max, kept[i]) < 0) continue;
-      const long long at = row_of(a.block_table_out, a.max_pages_out, a.T_out, i);
-      if (at >= 0) dst[at * vecs + c0 + c] = x[u];
+  if (n_batches == 0) return;
+  fill(0);
+  __syncthreads();
+  load(0, cur);
+  for (int i = 0; i < n_batches; ++i) {
+    if (i + 1 < n_batches) {
+      if ((i + 1) % per_table == 0) {
+        fill((i + 1) / per_table);  // over the table before last: its last stores lie behind a barrier
+        __syncthreads();
+      }
+      load(i + 1, nxt);
     }
-  };
-  const int batch = rows * kMoveUnroll;
-  if (r0 < r1) load(r0, cur);
-  for (int r = r0; r < r1; r += batch) {
-    if (r + batch < r1) load(r + batch, nxt);
     __syncthreads();  // every load of this batch (and the next) comes before its stores
-    store(r, cur);
+    store(i, cur);
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) cur[u] = nxt[u];
   }
@@ -237,16 +279,18 @@ template <typename Vec>
 cudaError_t launch_move(const EvictArgs& a, long long row_bytes, int num_sms, cudaStream_t s) {
   const int vecs = (int)(row_bytes / sizeof(Vec));
   const long long bg = (long long)a.B * a.h_kv;
-  // column slices: 128 bytes where that gives every SM two blocks, down to 32 (a DRAM sector) where not
-  int slice = 128 / (int)sizeof(Vec);
+  // Column slices (a power of two of vectors). An in-place or paged move has only these to share: 128 bytes where
+  // that gives every SM two blocks, down to 32 (a DRAM sector) where not. A copy into another contiguous
+  // cache has no order and is cut along the rows instead: whole rows up to 256 bytes.
+  const bool ordered = a.in_place || a.block_table;
+  int slice = (ordered ? 128 : 256) / (int)sizeof(Vec);
   const int least = 32 / (int)sizeof(Vec);
   auto slices = [&](int w) { return (vecs + w - 1) / w; };
-  while (slice > least && bg * 2 * slices(slice) < 2ll * num_sms) slice /= 2;
+  while (ordered && slice > least && bg * 2 * slices(slice) < 2ll * num_sms) slice /= 2;
   while (slice > 1 && slice / 2 >= vecs) slice /= 2;
   const int n_slices = slices(slice);
-  // a copy into another contiguous cache has no order: cut it along the rows until the SMs have work
   int split = 1;
-  if (!a.in_place && !a.block_table) {
+  if (!ordered) {
     const int rows = kMoveThreads / slice * kMoveUnroll;
     const int most = (a.budget + rows - 1) / rows;
     const long long want = (16ll * num_sms + bg * 2 * n_slices - 1) / (bg * 2 * n_slices);
@@ -285,7 +329,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int d_h, int elem_bytes, int num
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const int keep = a.T_max < ev::kSelKeep ? a.T_max : ev::kSelKeep;
-  ev::kv_evict_select_kernel<<<(unsigned)(a.B * a.h_kv), ev::kSelThreads, (size_t)keep * 4, s>>>(a);
+  ev::kv_evict_select_kernel<<<(unsigned)(a.B * a.h_kv), ev::kSelThreads, (size_t)(keep + 3) / 4 * 16, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long row_bytes = (long long)d_h * elem_bytes;
