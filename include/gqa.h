@@ -310,6 +310,57 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
                            gqa_dtype dtype, void* stream);
 
 /*
+ * Modified scores: gqa_prefill_mod, gqa_prefill_backward_mod, gqa_decode_mod, gqa_decode_paged_mod take
+ * the arguments of the calls without _mod, and a gqa_score_mod (host memory, read during the call):
+ *   s = scale q.k;  with a softcap c > 0:  s = c tanh(s / c);  with slopes:  s = s - slope[a] |p - j|
+ * for query head a, the row's position p (q_start[b] + i, decode q_pos[b]) and the key's row j. The softmax, lse
+ * and the gradients are those of the modified score; slopes are constants (they get no gradient).
+ *   key_range  row i of sequence b sees only keys lo <= j < hi, (lo, hi) = key_range[b, i], within what the causal
+ *              mask, window and length leave. It writes a document mask (lo, hi the document's rows), a
+ *              bidirectional prefix (causal 0, hi the later of p + 1 and the prefix's end), or both. Rows need no order. lo < 0
+ *              means 0. A row without a key is written as zeros, lse = -inf, gradients 0, and is no error. K
+ *              and V rows outside the keys that a 128-row tile's rows see between them may hold anything.
+ *              bf16 prefill and backward work through the blocks between a tile's least and largest key.
+ * mod NULL, or nothing set in it: the plain call, bit for bit.
+ * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
+ * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. gqa_prefill_backward_mod needs
+ * gqa_prefill_backward_mod_workspace_size bytes with a key_range, gqa_prefill_backward's without. The
+ * decode calls take gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is
+ * negative, NaN or infinite.
+ */
+typedef struct {
+  float softcap;             /* > 0: cap of the scores; 0: none */
+  const float* alibi_slopes; /* device fp32[h_q], or NULL */
+  const int32_t* key_range;  /* device int32: prefill (B, S_q, 2), decode (B, 2); or NULL */
+} gqa_score_mod;
+
+size_t gqa_prefill_mod_workspace_size(int B, int h_q, int h_kv, int S_q);
+gqa_status gqa_prefill_mod(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                           const int32_t* q_start, const int32_t* kv_len, const gqa_score_mod* mod,
+                           int B, int h_q, int h_kv, int S_q, int T_max, int d_h, float scale,
+                           int causal, int window, gqa_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t gqa_prefill_backward_mod_workspace_size(int B, int h_q, int h_kv, int S_q);
+gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const void* v_cache, const void* o,
+                                    const void* d_o, const float* lse, void* dq, void* dk, void* dv,
+                                    const int32_t* q_start, const int32_t* kv_len,
+                                    const gqa_score_mod* mod, int B, int h_q, int h_kv, int S_q,
+                                    int T_max, int d_h, float scale, int causal, int window,
+                                    gqa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+gqa_status gqa_decode_mod(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                          const int32_t* kv_len, const int32_t* q_pos, const gqa_score_mod* mod, int B,
+                          int h_q, int h_kv, int T_max, int d_h, float scale, int window,
+                          gqa_dtype dtype, void* workspace, size_t workspace_bytes, int num_splits,
+                          void* stream);
+gqa_status gqa_decode_paged_mod(const void* q, const void* k_pages, const void* v_pages, void* o,
+                                float* lse, const int32_t* kv_len, const int32_t* q_pos,
+                                const int32_t* block_table, const gqa_score_mod* mod, int B, int h_q,
+                                int h_kv, int num_pages, int page_size, int max_pages, int d_h,
+                                float scale, int window, gqa_dtype dtype, void* workspace,
+                                size_t workspace_bytes, int num_splits, void* stream);
+
+/*
  * gqa_rope - rotary position embedding of the rows x (B, h, S, d). Pair i of the d_rot elements from
  * `offset` on turns by the angle p * inv_freq[i] of the row's position p; the other elements are
  * copied. With c = scale * cos, s = scale * sin of the angle and m = d_rot / 2:

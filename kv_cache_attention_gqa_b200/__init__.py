@@ -16,6 +16,7 @@ from ._lib import (  # noqa: F401
     decode_paged,
     decode_workspace_size,
     get_device_error,
+    key_ranges,
     kv_append,
     kv_append_paged,
     kv_evict,

@@ -35,6 +35,15 @@ DEVERR_NAMES = {0: "none", 1: "kv_len out of range", 2: "position out of range",
 # name -> (restype, argtypes), mirroring include/gqa.h
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _L3 = ctypes.POINTER(ctypes.c_int64)  # three strides (host memory)
+
+
+class _ScoreMod(ctypes.Structure):
+    """gqa_score_mod"""
+
+    _fields_ = [("softcap", _F), ("alibi_slopes", _P), ("key_range", _P)]
+
+
+_M = ctypes.POINTER(_ScoreMod)
 SIGNATURES = {
     "gqa_prefill": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P]),
     "gqa_decode_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
@@ -60,6 +69,14 @@ SIGNATURES = {
                                   _P, _Z, _P]),
     "kv_evict": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "kv_evict_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "gqa_prefill_mod_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "gqa_prefill_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _P, _Z, _P]),
+    "gqa_prefill_backward_mod_workspace_size": (_Z, [_I, _I, _I, _I]),
+    "gqa_prefill_backward_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _I,
+                                      _F, _I, _I, _I, _P, _Z, _P]),
+    "gqa_decode_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _F, _I, _I, _P, _Z, _I, _P]),
+    "gqa_decode_paged_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                  _I, _P, _Z, _I, _P]),
     "gqa_get_device_error": (_I, [ctypes.POINTER(_I), _P]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
     "gqa_version": (ctypes.c_char_p, []),
@@ -209,11 +226,47 @@ def kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tensor,
                                        _ptr(pos_t), B, h_kv, k_new.shape[2], T_max, d_h, dt, _stream()))
 
 
+def _score_mod(softcap: float, alibi_slopes, key_range, h_q: int, shape):
+    """gqa_score_mod of a call's keyword arguments, or None when none is set."""
+    if not softcap and alibi_slopes is None and key_range is None:
+        return None
+    _need_cuda(alibi_slopes, key_range)
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or tuple(alibi_slopes.shape) != (h_q,)):
+        raise ValueError(f"alibi_slopes must be float32 of shape ({h_q},)")
+    if key_range is not None and (key_range.dtype != torch.int32 or tuple(key_range.shape) != shape):
+        raise ValueError(f"key_range must be int32 of shape {shape}")
+    return _ScoreMod(float(softcap), _ptr(alibi_slopes), _ptr(key_range))
+
+
+def key_ranges(doc_ids: torch.Tensor, *, prefix_len=None, causal: bool = True) -> torch.Tensor:
+    """``key_range`` (B, S, 2) int32 for documents packed into the S cached rows of each sequence: neighbours with equal
+    ``doc_ids`` (B, S) are one document, a negative id is padding (its rows see nothing). Rows see the keys of their
+    document at and before them (``causal``), or all of them; ``prefix_len`` (an int, or ids' shape: the length for
+    each row's document): the first rows of a document are seen by all of it. Use with ``causal=False``."""
+    B, S = doc_ids.shape
+    at = torch.arange(S, device=doc_ids.device).expand(B, S)
+    new = torch.ones_like(doc_ids, dtype=torch.bool)
+    new[:, 1:] = doc_ids[:, 1:] != doc_ids[:, :-1]
+    lo = torch.where(new, at, 0).cummax(1).values
+    last = torch.ones_like(new)
+    last[:, :-1] = new[:, 1:]
+    hi = torch.where(last, at + 1, S).flip(1).cummin(1).values.flip(1)
+    if causal:
+        end = at + 1
+        if prefix_len is not None:
+            end = torch.maximum(end, torch.minimum(lo + prefix_len, hi))
+        hi = end
+    pad = doc_ids < 0
+    return torch.stack([lo.masked_fill(pad, 0), hi.masked_fill(pad, 0)], -1).to(torch.int32)
+
+
 def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, q_start=None,
             kv_len=None, scale: float | None = None, causal: bool = True, window: int = 0,
-            out=None, return_lse: bool = False):
+            softcap: float = 0.0, alibi_slopes=None, key_range=None, out=None, return_lse: bool = False):
     """Grouped-query attention of q (B, h_q, S_q, d_h) over the cache (B, h_kv, T_max, d_h).
-    ``window`` > 0: sliding window, row at position p sees keys p - window < j <= p."""
+    ``window`` > 0: sliding window, row at position p sees keys p - window < j <= p. ``softcap`` > 0: scores s become
+    softcap tanh(s / softcap); ``alibi_slopes`` (h_q,) fp32: slope |p - j| is subtracted; ``key_range`` (B, S_q, 2)
+    int32: a row sees only keys lo <= j < hi (see ``key_ranges``)."""
     _need_cuda(q, k_cache, v_cache, out)
     B, h_q, S_q, d_h = q.shape
     Bk, h_kv, T_max, dk = k_cache.shape
@@ -227,6 +280,15 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, q_
     qs = _int_vec(q_start, B, q.device, "q_start")
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     scale = _scale(scale)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, S_q, 2))
+    if mod is not None:
+        # the ranges' hulls: scratch of this call (a capture keeps it in its own pool)
+        need = _lib.gqa_prefill_mod_workspace_size(B, h_q, h_kv, S_q) if key_range is not None else 0
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        _check("gqa_prefill_mod", _lib.gqa_prefill_mod(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(qs), _ptr(kl), mod, B, h_q, h_kv, S_q,
+            T_max, d_h, scale, 1 if causal else 0, int(window), dt, _ptr(ws), need, _stream()))
+        return (out, lse) if return_lse else out
     _check("gqa_prefill", _lib.gqa_prefill(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse),
                                            _ptr(qs), _ptr(kl), B, h_q, h_kv, S_q, T_max, d_h, scale,
                                            1 if causal else 0, int(window), dt, _stream()))
@@ -261,10 +323,12 @@ def workspace(nbytes: int, device) -> torch.Tensor:
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, kv_len=None,
-           q_pos=None, scale: float | None = None, window: int = 0, num_splits: int = 0, out=None,
+           q_pos=None, scale: float | None = None, window: int = 0, num_splits: int = 0,
+           softcap: float = 0.0, alibi_slopes=None, key_range=None, out=None,
            return_lse: bool = False, ws: torch.Tensor | None = None):
     """Split-KV decode of q (B, h_q, d_h) over the cache (B, h_kv, T_max, d_h).
-    ``window`` > 0: sliding window, the query at q_pos sees keys q_pos - window < j <= q_pos."""
+    ``window`` > 0: sliding window, the query at q_pos sees keys q_pos - window < j <= q_pos.
+    ``softcap``, ``alibi_slopes``: as in ``prefill``; ``key_range`` (B, 2): the keys each sequence sees."""
     _need_cuda(q, k_cache, v_cache, out)
     B, h_q, d_h = q.shape
     Bk, h_kv, T_max, dk = k_cache.shape
@@ -284,6 +348,12 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, kv_
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
     if ws is None:
         ws = workspace(need, q.device)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    if mod is not None:
+        _check("gqa_decode_mod", _lib.gqa_decode_mod(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), mod, B, h_q, h_kv, T_max,
+            d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
+        return (out, lse) if return_lse else out
     _check("gqa_decode", _lib.gqa_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse),
                                          _ptr(kl), _ptr(qp), B, h_q, h_kv, T_max, d_h, scale,
                                          int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
@@ -333,11 +403,11 @@ def _pool_shape(k_pages: torch.Tensor, v_pages: torch.Tensor):
 
 def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table, *,
                  kv_len=None, q_pos=None, scale: float | None = None, window: int = 0,
-                 num_splits: int = 0, out=None, return_lse: bool = False,
-                 ws: torch.Tensor | None = None):
+                 num_splits: int = 0, softcap: float = 0.0, alibi_slopes=None, key_range=None, out=None,
+                 return_lse: bool = False, ws: torch.Tensor | None = None):
     """Split-KV decode of q (B, h_q, d_h) over a paged cache: pools (num_pages, h_kv, page_size,
     d_h) and block_table (B, max_pages) int32; position t of sequence b is row t % page_size of
-    page block_table[b, t // page_size]."""
+    page block_table[b, t // page_size]. Modified scores as in ``decode``."""
     _need_cuda(q, k_pages, v_pages, out)
     B, h_q, d_h = q.shape
     num_pages, h_kv, page_size, dk = _pool_shape(k_pages, v_pages)
@@ -360,6 +430,13 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
     if ws is None:
         ws = workspace(need, q.device)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    if mod is not None:
+        _check("gqa_decode_paged_mod", _lib.gqa_decode_paged_mod(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), _ptr(bt), mod, B, h_q,
+            h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits,
+            _stream()))
+        return (out, lse) if return_lse else out
     _check("gqa_decode_paged", _lib.gqa_decode_paged(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), _ptr(bt),
         B, h_q, h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws),
@@ -388,10 +465,11 @@ def kv_append_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_new: torch.T
 def prefill_backward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, o: torch.Tensor,
                      d_o: torch.Tensor, lse: torch.Tensor, *, q_start=None, kv_len=None,
                      scale: float | None = None, causal: bool = True, window: int = 0,
+                     softcap: float = 0.0, alibi_slopes=None, key_range=None,
                      ws: torch.Tensor | None = None):
     """Gradients (dq, dk, dv) of ``prefill`` for the upstream gradient ``d_o``; ``o`` and ``lse``
-    are the forward's outputs (``prefill(..., return_lse=True)``). dk, dv have the cache's shape,
-    zero past each kv_len."""
+    are the forward's outputs (``prefill(..., return_lse=True)``, the same arguments). dk, dv have the cache's
+    shape, zero past each kv_len. ``alibi_slopes`` are constants."""
     _need_cuda(q, k_cache, v_cache, o, d_o, lse)
     B, h_q, S_q, d_h = q.shape
     Bk, h_kv, T_max, dk_ = k_cache.shape
@@ -408,9 +486,17 @@ def prefill_backward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     qs = _int_vec(q_start, B, q.device, "q_start")
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     scale = _scale(scale)
-    need = _lib.gqa_prefill_backward_workspace_size(B, h_q, S_q)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, S_q, 2))
+    need = (_lib.gqa_prefill_backward_workspace_size(B, h_q, S_q) if key_range is None
+            else _lib.gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q))
     if ws is None or _ws_bytes(ws) < need:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if mod is not None:
+        _check("gqa_prefill_backward_mod", _lib.gqa_prefill_backward_mod(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(qs),
+            _ptr(kl), mod, B, h_q, h_kv, S_q, T_max, d_h, scale, 1 if causal else 0, int(window), dt, _ptr(ws),
+            _ws_bytes(ws), _stream()))
+        return dq, dk, dv
     _check("gqa_prefill_backward", _lib.gqa_prefill_backward(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(dq), _ptr(dk),
         _ptr(dv), _ptr(qs), _ptr(kl), B, h_q, h_kv, S_q, T_max, d_h, scale, 1 if causal else 0,

@@ -81,6 +81,18 @@ bool encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* d
 bool valid_scale(float s) { return isfinite(s) && s >= 0.f; }
 float resolve_scale(float s, int d) { return s == 0.f ? (float)(1.0 / sqrt((double)d)) : s; }
 
+// modified scores: a cap finite and > 0, or 0 for none
+bool valid_mod(const gqa_score_mod* m) { return !m || (isfinite(m->softcap) && m->softcap >= 0.f); }
+ScoreMod score_mod(const gqa_score_mod* m) {
+  ScoreMod s;
+  if (m) {
+    s.softcap = m->softcap;
+    s.slopes = m->alibi_slopes;
+    s.range = m->key_range;
+  }
+  return s;
+}
+
 gqa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA; }
 
 }  // namespace
@@ -114,13 +126,15 @@ gqa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
                        const int32_t* kv_len, const int32_t* q_pos, int B, int h_q, int h_kv,
                        int T_max, int d_h, float scale, int window, gqa_dtype dtype, void* workspace,
                        size_t workspace_bytes, int num_splits, void* stream,
-                       const int32_t* block_table, int max_pages, int page_size, int num_pages) {
+                       const int32_t* block_table, int max_pages, int page_size, int num_pages,
+                       const gqa_score_mod* mod = nullptr) {
   using namespace gqa;
   const long long cache_rows =
       block_table ? (long long)num_pages * h_kv * page_size : (long long)B * h_kv * T_max;
   const gqa_status st = decode_check_args(q, k_cache, v_cache, o, B, h_q, h_kv, T_max, d_h, scale,
                                           window, dtype, num_splits, cache_rows);
   if (st != GQA_OK) return st;
+  if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
   scale = resolve_scale(scale, d_h);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GQA_ERR_WORKSPACE;
   // the workspace check needs no device query when num_splits is given
@@ -154,6 +168,7 @@ gqa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.expire_wait = g_expire_waits.load(std::memory_order_relaxed);
+  a.mod = score_mod(mod);
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -421,6 +436,20 @@ gqa_status gqa_prefill(const void* q, const void* k_cache, const void* v_cache, 
                        float* lse, const int32_t* q_start, const int32_t* kv_len,
                        int B, int h_q, int h_kv, int S_q, int T_max, int d_h,
                        float scale, int causal, int window, gqa_dtype dtype, void* stream) {
+  return gqa_prefill_mod(q, k_cache, v_cache, o, lse, q_start, kv_len, nullptr, B, h_q, h_kv, S_q, T_max, d_h,
+                         scale, causal, window, dtype, nullptr, 0, stream);
+}
+
+size_t gqa_prefill_mod_workspace_size(int B, int h_q, int h_kv, int S_q) {
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || S_q <= 0 || h_q % h_kv != 0) return 0;
+  return (prefill_hull_bytes(B, h_q, h_kv, S_q) + 255) / 256 * 256;
+}
+
+gqa_status gqa_prefill_mod(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                           const int32_t* q_start, const int32_t* kv_len, const gqa_score_mod* mod,
+                           int B, int h_q, int h_kv, int S_q, int T_max, int d_h, float scale,
+                           int causal, int window, gqa_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
   if (!q || !k_cache || !v_cache || !o) return GQA_ERR_INVALID_ARG;
   // a window is measured back from each row's own position, so it needs the causal mask
   if (window < 0 || (window > 0 && causal != 1)) return GQA_ERR_INVALID_ARG;
@@ -437,6 +466,11 @@ gqa_status gqa_prefill(const void* q, const void* k_cache, const void* v_cache, 
     if ((long long)B * h_kv * T_max >= (1ll << 31) || (long long)B * h_q * S_q >= (1ll << 31))
       return GQA_ERR_UNSUPPORTED;
   }
+  if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
+  if (dtype == GQA_BF16 && mod && mod->key_range &&
+      (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+       workspace_bytes < gqa_prefill_mod_workspace_size(B, h_q, h_kv, S_q)))
+    return GQA_ERR_WORKSPACE;
   PrefillArgs a;
   a.q = q;
   a.k = k_cache;
@@ -455,6 +489,8 @@ gqa_status gqa_prefill(const void* q, const void* k_cache, const void* v_cache, 
   a.causal = causal;
   a.window = window;
   a.expire_wait = g_expire_waits.load(std::memory_order_relaxed);
+  a.mod = score_mod(mod);
+  a.workspace = workspace;
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -489,6 +525,23 @@ gqa_status gqa_prefill_backward(const void* q, const void* k_cache, const void* 
                                 int B, int h_q, int h_kv, int S_q, int T_max, int d_h, float scale,
                                 int causal, int window, gqa_dtype dtype, void* workspace,
                                 size_t workspace_bytes, void* stream) {
+  return gqa_prefill_backward_mod(q, k_cache, v_cache, o, d_o, lse, dq, dk, dv, q_start, kv_len, nullptr, B, h_q,
+                                  h_kv, S_q, T_max, d_h, scale, causal, window, dtype, workspace, workspace_bytes,
+                                  stream);
+}
+
+size_t gqa_prefill_backward_mod_workspace_size(int B, int h_q, int h_kv, int S_q) {
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || S_q <= 0 || h_q % h_kv != 0) return 0;
+  return gqa_prefill_backward_workspace_size(B, h_q, S_q) + (backward_hull_bytes(B, h_q, h_kv, S_q) + 255) / 256 * 256;
+}
+
+gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const void* v_cache, const void* o,
+                                    const void* d_o, const float* lse, void* dq, void* dk, void* dv,
+                                    const int32_t* q_start, const int32_t* kv_len,
+                                    const gqa_score_mod* mod, int B, int h_q, int h_kv, int S_q,
+                                    int T_max, int d_h, float scale, int causal, int window,
+                                    gqa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
   if (!q || !k_cache || !v_cache || !o || !d_o || !lse || !dq || !dk || !dv) return GQA_ERR_INVALID_ARG;
   if (B <= 0 || h_q <= 0 || h_kv <= 0 || S_q <= 0 || T_max <= 0 || d_h <= 0) return GQA_ERR_INVALID_ARG;
   if (h_q % h_kv != 0 || !valid_scale(scale)) return GQA_ERR_INVALID_ARG;
@@ -500,7 +553,9 @@ gqa_status gqa_prefill_backward(const void* q, const void* k_cache, const void* 
   if (dtype == GQA_BF16 && d_h != 64 && d_h != 128) return GQA_ERR_UNSUPPORTED;
   if ((long long)B * h_kv * T_max >= (1ll << 31) || (long long)B * h_q * S_q >= (1ll << 31))
     return GQA_ERR_UNSUPPORTED;
-  const size_t need = gqa_prefill_backward_workspace_size(B, h_q, S_q);
+  if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
+  const size_t base = gqa_prefill_backward_workspace_size(B, h_q, S_q);
+  const size_t need = mod && mod->key_range ? gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q) : base;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
     return GQA_ERR_WORKSPACE;
   BackwardArgs a;
@@ -524,10 +579,12 @@ gqa_status gqa_prefill_backward(const void* q, const void* k_cache, const void* 
   a.scale = scale;
   a.causal = causal;
   a.window = window;
-  const size_t half = (need - 256) / 2;
+  const size_t half = (base - 256) / 2;
   a.lse2 = reinterpret_cast<float*>(workspace);
   a.drow = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + half);
   a.ticket = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(workspace) + 2 * half);
+  a.mod = score_mod(mod);
+  a.hull = reinterpret_cast<uint8_t*>(workspace) + base;
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -883,6 +940,30 @@ gqa_status kv_evict_paged(void* k_pages, void* v_pages, const int32_t* block_tab
   a.page_size = page_size;
   a.num_pages = num_pages;
   return evict_impl(a, d_h, dtype, stream);
+}
+
+gqa_status gqa_decode_mod(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                          const int32_t* kv_len, const int32_t* q_pos, const gqa_score_mod* mod, int B,
+                          int h_q, int h_kv, int T_max, int d_h, float scale, int window,
+                          gqa_dtype dtype, void* workspace, size_t workspace_bytes, int num_splits,
+                          void* stream) {
+  return decode_impl(q, k_cache, v_cache, o, lse, kv_len, q_pos, B, h_q, h_kv, T_max, d_h, scale, window, dtype,
+                     workspace, workspace_bytes, num_splits, stream, nullptr, 0, 0, 0, mod);
+}
+
+gqa_status gqa_decode_paged_mod(const void* q, const void* k_pages, const void* v_pages, void* o,
+                                float* lse, const int32_t* kv_len, const int32_t* q_pos,
+                                const int32_t* block_table, const gqa_score_mod* mod, int B, int h_q,
+                                int h_kv, int num_pages, int page_size, int max_pages, int d_h,
+                                float scale, int window, gqa_dtype dtype, void* workspace,
+                                size_t workspace_bytes, int num_splits, void* stream) {
+  if (!block_table || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0) return GQA_ERR_UNSUPPORTED;
+  const long long T_max = (long long)max_pages * page_size;
+  if (T_max >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
+  return decode_impl(q, k_pages, v_pages, o, lse, kv_len, q_pos, B, h_q, h_kv, (int)T_max, d_h, scale, window,
+                     dtype, workspace, workspace_bytes, num_splits, stream, block_table, max_pages, page_size,
+                     num_pages, mod);
 }
 
 }  // extern "C"

@@ -31,6 +31,9 @@
 //               S = Q K^T, dP = dO V^T (A = the tile's Q / dO rows, copied once into TMEM;
 //               B = K / V from shared memory), then dS -> bf16 into TMEM, dQ += dS K (A = dS from
 //               TMEM, B = K, MN-major view).
+// kMod kernels (modified scores): P comes from the capped and biased score and dS gains the cap's derivative
+// 1 - tanh^2; the query blocks of a key tile and the key blocks of a dq tile follow the rows' key ranges, whose
+// hulls per row block two small kernels in front work out (row_hull).
 // Masks: on blocks that straddle the diagonal, the window or the length, each elementwise thread
 // compares indices with one pair of 32-bit bounds fixed for the block: the query columns that see
 // its key (dkdv) or the keys its row sees (dq).
@@ -74,6 +77,8 @@ struct BArgs {
   int n_items;              // dkdv tiles + dq tiles
   int* ticket;              // items handed out past the first gridDim.x (reset by rowterm)
   unsigned* err;
+  ModArgs mod;              // kMod kernels only; mod.hull: of the dq tiles
+  const int4* hull64;       // kMod with ranges: of the 64-row query blocks (dkdv)
 };
 
 // Bounded mbarrier wait shared by all roles: gives up after 2 s (or when another thread of the
@@ -224,7 +229,8 @@ struct KvCfg {
   static constexpr int kOffV = kKTile;
   static constexpr int kOffQ = 2 * kKTile;                        // + stage * 2 * kQTile
   static constexpr int kOffStat = kOffQ + kKvStages * 2 * kQTile;  // stages x (lse2[64], D[64])
-  static constexpr int kOffBar = kOffStat + kKvStages * 2 * kKvBQ * 4;
+  static constexpr int kOffRange = kOffStat + kKvStages * 2 * kKvBQ * 4;  // kMod: stages x (lo[64], hi[64])
+  static constexpr int kOffBar = kOffRange + kKvStages * 2 * kKvBQ * 4;
   static constexpr int kSmem = (kOffBar + 256 + 1024) > 120 * 1024 ? kOffBar + 256 + 1024 : 120 * 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -239,7 +245,7 @@ enum {
 };
 
 // One CTA of the dK / dV pass for tile `tile` (sequence, KV head, key block).
-template <int D>
+template <int D, bool kMod>
 __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorMap& tmdo,
                                          const CUtensorMap& tmk, const CUtensorMap& tmv, const BArgs& a,
                                          int tile, uint32_t tmem) {
@@ -251,6 +257,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
   // the abort flag sits after the barriers (the TMEM address is the kernel's, held across items)
   volatile int* abort = reinterpret_cast<volatile int*>(bars + kKvBars) + 1;
   float* stat = reinterpret_cast<float*>(smem + C::kOffStat);  // [stage][lse2 64 | D 64]
+  int* srange = reinterpret_cast<int*>(smem + C::kOffRange);   // [stage][lo 64 | hi 64]
   const uint32_t sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
   auto sQ = [&](int st) { return smem_u32(smem + C::kOffQ + st * 2 * C::kQTile); };
   auto sDO = [&](int st) { return smem_u32(smem + C::kOffQ + st * 2 * C::kQTile + C::kQTile); };
@@ -278,6 +285,34 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
         const long long last_q = k_last + a.window - 1 - qs;  // latest row that can see k_last
         qb_hi = last_q < 0 ? -1 : (int)min((long long)qb_hi, last_q / kKvBQ);
       }
+    }
+  }
+  if constexpr (kMod) {
+    if (a.mod.range) {
+      // the first and the last query block whose rows' ranges reach into these keys
+      __shared__ int s_lo, s_hi;
+      if (threadIdx.x == 0) {
+        s_lo = 0x7fffffff;
+        s_hi = -1;
+      }
+      cta_sync();
+      const int k1 = min(k0 + kBK, kv);
+      int lo = 0x7fffffff, hi = -1;
+      for (int qb = qb_lo + (int)threadIdx.x; qb <= qb_hi; qb += kKvThreads) {
+        const int4 h = a.hull64[(long long)b * n_qb + qb];
+        if (h.x < k1 && h.y > k0) {
+          lo = min(lo, qb);
+          hi = qb;
+        }
+      }
+      if (hi >= 0) {
+        atomicMin(&s_lo, lo);
+        atomicMax(&s_hi, hi);
+      }
+      cta_sync();
+      qb_lo = s_lo;
+      qb_hi = s_hi;
+      cta_sync();  // read before the next item's first write
     }
   }
   const int nq = qb_hi >= qb_lo ? qb_hi - qb_lo + 1 : 0;
@@ -343,6 +378,11 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
         const long long row = (long long)z * a.S_q + qi;
         sl[c] = qi < a.S_q ? -a.lse2[row] : -INFINITY;  // stored negated for the fused FMAs
         sl[kKvBQ + c] = qi < a.S_q ? -a.drow[row] : 0.f;
+        if (kMod && a.mod.range) {
+          const int2 rg = qi < a.S_q ? a.mod.range[(long long)b * a.S_q + qi] : make_int2(0, 0);
+          srange[st * 2 * kKvBQ + c] = rg.x;
+          srange[st * 2 * kKvBQ + kKvBQ + c] = rg.y;
+        }
       }
       mbar_arrive(bar(kQFull + st));
       last[st] = n;
@@ -433,6 +473,13 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
       const bool need_mask = k0 + kBK > kv || col0 + 32 > a.S_q ||
                              (a.causal && (long long)k0 + kBK - 1 > pos0) ||
                              (a.window > 0 && (long long)k0 <= pos0 + 31 - a.window);
+      // kMod: per-row ranges, unless these keys lie in every row's
+      bool ranged = false;
+      const int* rl = srange + st * 2 * kKvBQ + half * 32;
+      if (kMod && a.mod.range) {
+        const int4 h = a.hull64[(long long)b * n_qb + qb];
+        ranged = h.z > k0 || h.w < k0 + kBK;
+      }
       tc::fence_after_sync();
       uint32_t sv[32], dv[32];
       tc::ld32(lane_addr + 64 * bf + 32 * half, sv);
@@ -449,14 +496,33 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
         c_hi = key < kv ? (int)(hi < 0 ? 0 : hi) : 0;
       }
       uint32_t pp[16], pd[16];
-      const float2 c2 = make_float2(a.sl2, a.sl2);
+      const bool cap = kMod && a.mod.cap2 > 0.f;
+      float* const sf = reinterpret_cast<float*>(sv);
+      if (cap) tanh_scores<32>(sf, a.mod.k1);
+      const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
+      // kMod: bias per key of distance (base 2) of this block's head, and the distance of its first row
+      const float slope2 = kMod && a.mod.slopes ? a.mod.slopes[head_of(it)] * kLog2e : 0.f;
+      const float away = (float)(pos0 - key);
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
         const float2 nl = *reinterpret_cast<const float2*>(sl + x);          // -lse2 of the two rows
         const float2 nd = *reinterpret_cast<const float2*>(sl + kKvBQ + x);  // -D of the two rows
-        const float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
+        float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
+        if (kMod && a.mod.slopes) {
+          arg.x = fmaf(-slope2, fabsf(away + (float)x), arg.x);
+          arg.y = fmaf(-slope2, fabsf(away + (float)(x + 1)), arg.y);
+        }
         float2 p = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
         float2 ds = mul2(p, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd));
+        if (cap) {
+          const float2 t = make_float2(sf[x], sf[x + 1]);
+          ds = mul2(ds, fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
+        }
+        if (kMod && ranged) {
+          const int2 lo = *reinterpret_cast<const int2*>(rl + x), hi = *reinterpret_cast<const int2*>(rl + kKvBQ + x);
+          if (key < lo.x || key >= hi.x) p.x = ds.x = 0.f;
+          if (key < lo.y || key >= hi.y) p.y = ds.y = 0.f;
+        }
         if (need_mask) {
           if (x < c_lo || x >= c_hi) p.x = ds.x = 0.f;
           if (x + 1 < c_lo || x + 1 >= c_hi) p.y = ds.y = 0.f;
@@ -556,9 +622,11 @@ enum {
 // j0 .. j0 + nb - 1 its rows see.
 struct DqTile {
   int b, g, hb, q0, nh, kv, qs, j0, nb;
+  int lo_key, hi_key;  // kMod: keys [lo_key, hi_key) that some row of the tile sees
   long long pos_min, pos_max;
 };
 
+template <bool kMod>
 __device__ __forceinline__ DqTile dq_tile(const BArgs& a, int tile) {
   DqTile t;
   const int per = a.B * a.h_kv * a.hblocks;
@@ -578,6 +646,26 @@ __device__ __forceinline__ DqTile dq_tile(const BArgs& a, int tile) {
   t.pos_max = (long long)t.qs + min(t.q0 + a.P, a.S_q) - 1;
   t.j0 = 0;
   t.nb = 0;
+  t.lo_key = t.hi_key = 0;
+  if constexpr (kMod) {
+    if (!valid) return t;
+    long long l = 0, h = t.kv;
+    if (a.causal) {
+      if (t.pos_max + 1 < h) h = t.pos_max + 1;
+      if (a.window > 0 && t.pos_min - a.window + 1 > l) l = t.pos_min - a.window + 1;
+    }
+    if (a.mod.hull) {
+      const int4 hl = a.mod.hull[(long long)t.b * a.n_qt + qt];
+      if (hl.x > l) l = hl.x;
+      if (hl.y < h) h = hl.y;
+    }
+    if (l >= h) return t;
+    t.lo_key = (int)l;
+    t.hi_key = (int)h;
+    t.j0 = t.lo_key / kQBK;
+    t.nb = (t.hi_key + kQBK - 1) / kQBK - t.j0;
+    return t;
+  }
   if (valid) {
     int end = (t.kv + kQBK - 1) / kQBK;
     if (a.causal) {
@@ -602,7 +690,7 @@ __device__ __forceinline__ DqTile dq_tile(const BArgs& a, int tile) {
 // which overwrites the accumulator, waits for dS that those warps produce after reading it out.
 // The producer hands each tile's number to the other roles through `s_items` (two slots), and a
 // number past the last item ends the run.
-template <int D>
+template <int D, bool kMod>
 __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap& tmdo,
                                        const CUtensorMap& tmk, const CUtensorMap& tmv, const BArgs& a,
                                        int item0, int n_dkdv, uint32_t tmem, volatile int* s_items) {
@@ -660,7 +748,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         break;
       }
       const int tile = item - n_dkdv;
-      const DqTile t = dq_tile(a, tile);
+      const DqTile t = dq_tile<kMod>(a, tile);
       s_items[n & 1] = tile;
       const int next = (int)gridDim.x + atomicAdd(a.ticket, 1);  // the next item, fetched early
       const int zq = t.b * a.h_q + t.g * a.r + t.hb * a.H;
@@ -719,7 +807,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       if (!(ok = wait(kQdQ, (uint32_t)(n & 1)))) break;
       const int tile = item_at(n);
       if (tile < 0) break;
-      const DqTile t = dq_tile(a, tile);
+      const DqTile t = dq_tile<kMod>(a, tile);
       // this tile's Q and dO in TMEM; only then is the release below allowed: it lets the
       // elementwise warps reach the next tile's copy, and this warp must not be two phases of
       // kQT behind when they do
@@ -801,7 +889,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       ok = __all_sync(0xffffffffu, ok);
       const int tile = ok ? item_at(n) : -1;
       if (tile < 0) break;
-      const DqTile t = dq_tile(a, tile);
+      const DqTile t = dq_tile<kMod>(a, tile);
       const int qi = t.q0 + p;
       const bool store_row = h < t.nh && row < a.H * a.P && qi < a.S_q;
       const long long srow = ((long long)t.b * a.h_q + t.g * a.r + t.hb * a.H + h) * a.S_q + qi;
@@ -810,9 +898,18 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       const float dr = store_row ? a.drow[srow] : 0.f;
       // keys [k_first, k_last] this row sees (length, causal and window limits as 32-bit bounds)
       const long long kl = a.causal && pos < t.kv - 1 ? pos : (long long)t.kv - 1;
-      const int k_last = (int)kl;
+      int k_last = (int)kl;
       const long long kf = a.window > 0 ? pos - a.window + 1 : 0;
-      const int k_first = kf < 0 ? 0 : (kf > 0x7fffffffLL ? 0x7fffffff : (int)kf);
+      int k_first = kf < 0 ? 0 : (kf > 0x7fffffffLL ? 0x7fffffff : (int)kf);
+      float slope2 = 0.f;  // kMod: bias per key of distance, base 2
+      if (kMod && store_row) {
+        if (a.mod.range) {
+          const int2 rg = a.mod.range[(long long)t.b * a.S_q + qi];
+          k_first = max(k_first, rg.x);
+          k_last = min(k_last, rg.y - 1);
+        }
+        if (a.mod.slopes) slope2 = a.mod.slopes[t.g * a.r + t.hb * a.H + h] * kLog2e;
+      }
       // this row of Q (half 0) or dO (half 1): shared memory (128-byte swizzled) -> TMEM. The
       // previous tile's S and dP MMAs, which read these columns, are complete (this warp saw the
       // scores of its last block).
@@ -854,20 +951,34 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         if (!ok) break;
         const int blk0 = (t.j0 + j) * kQBK;
         const int key0 = blk0 + half * 32;  // first key of this half
-        const bool need_mask = (a.causal && (long long)key0 + 31 > t.pos_min) || key0 + 32 > t.kv ||
-                               (a.window > 0 && (long long)key0 <= t.pos_max - a.window);
+        const bool need_mask = kMod ? store_row && (key0 < k_first || key0 + 31 > k_last)
+                                    : (a.causal && (long long)key0 + 31 > t.pos_min) || key0 + 32 > t.kv ||
+                                          (a.window > 0 && (long long)key0 <= t.pos_max - a.window);
         tc::fence_after_sync();
         uint32_t sv[32], dv[32];
         tc::ld32(lane_addr + 64 * bf + 32 * half, sv);
         tc::ld32(lane_addr + 128 + 64 * bf + 32 * half, dv);
         tc::wait_ld();
         uint32_t pd[16];
-        const float2 c2 = make_float2(a.sl2, a.sl2), nl = make_float2(-lse2, -lse2), nd2 = make_float2(-dr, -dr);
+        const bool cap = kMod && a.mod.cap2 > 0.f;
+        float* const sf = reinterpret_cast<float*>(sv);
+        if (cap) tanh_scores<32>(sf, a.mod.k1);
+        const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
+        const float2 nl = make_float2(-lse2, -lse2), nd2 = make_float2(-dr, -dr);
+        const float away = (float)(key0 - pos);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
-          const float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
+          float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
+          if (kMod && a.mod.slopes) {
+            arg.x = fmaf(-slope2, fabsf(away + (float)x), arg.x);
+            arg.y = fmaf(-slope2, fabsf(away + (float)(x + 1)), arg.y);
+          }
           const float2 pr = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
           float2 ds = mul2(pr, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd2));
+          if (cap) {
+            const float2 tt = make_float2(sf[x], sf[x + 1]);
+            ds = mul2(ds, fma2(make_float2(-tt.x, -tt.y), tt, make_float2(1.f, 1.f)));
+          }
           if (need_mask) {
             if (key0 + x < k_first || key0 + x > k_last) ds.x = 0.f;
             if (key0 + x + 1 < k_first || key0 + x + 1 > k_last) ds.y = 0.f;
@@ -877,11 +988,13 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         tc::st16(lane_addr + 64 * bf + 32 * half, pd);  // dS over this half's first columns of S
         // K rows no row of the tile may see (past kv_len: last block; below every row's window:
         // first block) get dS = 0 but may hold anything: zero them before dQ += dS K
-        const bool zero_tail = j == t.nb - 1 && blk0 + kQBK > t.kv;
-        const bool zero_head = j == 0 && a.window > 0 && (long long)blk0 < t.pos_min - a.window + 1;
+        const bool zero_tail = j == t.nb - 1 && blk0 + kQBK > (kMod ? t.hi_key : t.kv);
+        const bool zero_head =
+            j == 0 && (kMod ? blk0 < t.lo_key : a.window > 0 && (long long)blk0 < t.pos_min - a.window + 1);
         if ((zero_tail || zero_head) && et < kQBK) {
           const long long key = (long long)blk0 + et;  // this thread's K row of the block
-          if ((zero_tail && key >= t.kv) || (zero_head && key <= t.pos_min - a.window)) {
+          if (kMod ? key >= t.hi_key || key < t.lo_key
+                   : (zero_tail && key >= t.kv) || (zero_head && key <= t.pos_min - a.window)) {
             for (int ch = 0; ch < C::kNch; ++ch)
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
@@ -930,7 +1043,7 @@ struct BwCfg {
   static constexpr int kSmem = KvCfg<D>::kSmem > QCfg<D>::kSmem ? KvCfg<D>::kSmem : QCfg<D>::kSmem;
 };
 
-template <int D>
+template <int D, bool kMod>
 __global__ void __launch_bounds__(kKvThreads, 1)
     backward_kernel(const __grid_constant__ CUtensorMap tmq_rows, const __grid_constant__ CUtensorMap tmdo_rows,
                     const __grid_constant__ CUtensorMap tmk128, const __grid_constant__ CUtensorMap tmv128,
@@ -951,13 +1064,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   const uint32_t tmem = s_tmem;
   for (int item = blockIdx.x; item < a.n_items;) {
     if (item >= n_dkdv) {  // tickets only grow: every later item of this CTA is a dq tile too
-      dq_run<D>(tmq_tile, tmdo_tile, tmk64, tmv64, a, item, n_dkdv, tmem, s_items);
+      dq_run<D, kMod>(tmq_tile, tmdo_tile, tmk64, tmv64, a, item, n_dkdv, tmem, s_items);
       break;
     }
     // the next item's ticket, fetched while this item runs by a thread of the elementwise warps
     // (which wait for the first scores anyway); the item's closing barrier publishes it
     if (threadIdx.x == 64) s_next = (int)gridDim.x + atomicAdd(a.ticket, 1);
-    dkdv_cta<D>(tmq_rows, tmdo_rows, tmk128, tmv128, a, item, tmem);
+    dkdv_cta<D, kMod>(tmq_rows, tmdo_rows, tmk128, tmv128, a, item, tmem);
     item = s_next;
     cta_sync();  // every thread has read s_next before the next item writes it
   }
@@ -969,14 +1082,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kMod>
 cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(backward_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwCfg<D>::kSmem);
+    e = cudaFuncSetAttribute(backward_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
@@ -987,7 +1100,7 @@ cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cud
   BArgs q = p;
   q.n_items = (int)(n1 + n2);
   const long long ctas = n1 + n2 < num_sms ? n1 + n2 : num_sms;  // one CTA per SM
-  backward_kernel<D><<<(unsigned)ctas, kKvThreads, BwCfg<D>::kSmem, s>>>(
+  backward_kernel<D, kMod><<<(unsigned)ctas, kKvThreads, BwCfg<D>::kSmem, s>>>(
       tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], tm[6], tm[7], q, (int)n1);
   return cudaGetLastError();
 }
@@ -1042,9 +1155,32 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
   p.ticket = a.ticket;
   p.n_items = 0;
   p.err = a.err;
-  if (a.d_h == 128) return bw::launch_typed<128>(p, tmaps, num_sms, s);
-  if (a.d_h == 64) return bw::launch_typed<64>(p, tmaps, num_sms, s);
+  p.hull64 = nullptr;
+  if (a.mod.on()) {
+    p.mod = mod_args(a.mod, a.scale);
+    if (a.mod.range) {
+      const int n_qb = (a.S_q + bw::kKvBQ - 1) / bw::kKvBQ;
+      int4* hull = reinterpret_cast<int4*>(a.hull);
+      e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, p.n_qt, s);
+      if (e != cudaSuccess) return e;
+      int4* hull64 = hull + (size_t)a.B * p.n_qt;
+      e = launch_row_hull(a.mod.range, hull64, a.B, a.S_q, bw::kKvBQ, n_qb, s);
+      if (e != cudaSuccess) return e;
+      p.mod.hull = hull;
+      p.hull64 = hull64;
+    }
+    if (a.d_h == 128) return bw::launch_typed<128, true>(p, tmaps, num_sms, s);
+    if (a.d_h == 64) return bw::launch_typed<64, true>(p, tmaps, num_sms, s);
+    return cudaErrorInvalidValue;
+  }
+  if (a.d_h == 128) return bw::launch_typed<128, false>(p, tmaps, num_sms, s);
+  if (a.d_h == 64) return bw::launch_typed<64, false>(p, tmaps, num_sms, s);
   return cudaErrorInvalidValue;
+}
+
+size_t backward_hull_bytes(int B, int h_q, int h_kv, int S_q) {
+  const int P = 128 / prefill_heads_per_tile(h_q, h_kv);
+  return ((size_t)((S_q + P - 1) / P) + (S_q + bw::kKvBQ - 1) / bw::kKvBQ) * B * sizeof(int4);
 }
 
 }  // namespace gqa

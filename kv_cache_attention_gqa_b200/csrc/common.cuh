@@ -196,6 +196,72 @@ __device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
   return d;
 }
 
+// ---------------------------------------------------------------------------------------------
+// Modified scores: a cap by tanh, a bias that grows with distance, a range of keys per row
+// ---------------------------------------------------------------------------------------------
+// Kernel-side form of gqa_score_mod. With x = s k1 (s the raw product q.k, k1 = scale / cap) the base-2 score is
+// cap2 tanh(x) - slope2 |p - j|, cap2 = cap log2 e; without a cap it is s scale log2 e - slope2 |p - j|.
+struct ModArgs {
+  float k1 = 0.f, cap2 = 0.f;     // cap2 = 0: no cap
+  const float* slopes = nullptr;  // (h_q) natural-log slopes, or none
+  const int2* range = nullptr;    // (B, S_q) (decode: (B)) keys lo <= j < hi of each row, or none
+  const int4* hull = nullptr;     // per row block: least lo and largest hi of the rows that see any, then
+                                  // largest lo and least hi of all rows (see row_hull)
+};
+
+// Check mode: the score of one pair in natural units, `t` its tanh (for the gradient; 0 without a cap).
+__device__ __forceinline__ float mod_score(float dot, float scale, float cap, float slope, long long away, float* t) {
+  float s = dot * scale;
+  *t = 0.f;
+  if (cap > 0.f) {
+    *t = tanhf(s / cap);
+    s = cap * *t;
+  }
+  return slope != 0.f ? fmaf(-slope, fabsf((float)away), s) : s;
+}
+
+// tanh of a pair with |x| <= kTanhSmall: x times a polynomial in x^2 (least maximum relative error, fitted by
+// iterated reweighting: 2.9e-8; with fp32 rounding 1.6e-7).
+constexpr float kTanhSmall = 0.75f;
+__device__ __forceinline__ float2 pair_tanh_small(float2 x) {
+  const float2 z = pair_mul(x, x);
+  float2 p = pair_fma(make_float2(-0x1.3515aap-8f, -0x1.3515aap-8f), z, make_float2(0x1.40d8acp-6f, 0x1.40d8acp-6f));
+  p = pair_fma(p, z, make_float2(-0x1.b4ff60p-5f, -0x1.b4ff60p-5f));
+  p = pair_fma(p, z, make_float2(0x1.10e782p-3f, 0x1.10e782p-3f));
+  p = pair_fma(p, z, make_float2(-0x1.55545ap-2f, -0x1.55545ap-2f));
+  p = pair_fma(p, z, make_float2(0x1.000000p+0f, 0x1.000000p+0f));
+  return pair_mul(p, x);
+}
+// Any x: 1 - 2 / (e^(2x) + 1), absolute error below 3e-7 (of values up to 1, which the cap multiplies).
+__device__ __forceinline__ float tanh_any(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * 2.8853900817779268f) + 1.f));
+  return fmaf(-2.f, r, 1.f);
+}
+// t[k] = tanh(s[k] k1) for a thread's N scores, by the polynomial when every score of the warp is small enough (the
+// exponential unit then keeps to the softmax). Called by whole warps.
+template <int N>
+__device__ __forceinline__ void tanh_scores(float* s, float k1) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    m0 = fmaxf(m0, fabsf(s[k]));
+    m1 = fmaxf(m1, fabsf(s[k + 1]));
+  }
+  const float2 k2 = make_float2(k1, k1);
+  if (__all_sync(0xffffffffu, fmaxf(m0, m1) * k1 <= kTanhSmall)) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const float2 t = pair_tanh_small(pair_mul(make_float2(s[k], s[k + 1]), k2));
+      s[k] = t.x;
+      s[k + 1] = t.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = tanh_any(s[k] * k1);
+  }
+}
+
 // Barrier among `threads` threads (whole warps) on barrier `id`, aligned form: only where every
 // warp taking part arrives converged (no role or lane-divergent loop right before it; the
 // unaligned form, as in cta_sync, measured 2% slower on the decode_8k step).

@@ -143,6 +143,8 @@ struct KArgs {
   // multiple of 64 keys (every tile lies in one page), else 16 (every 16-key sub-tile does)
   int gran;
   int expire_wait;  // test hook: CTA 0's producer first waits on a barrier that nothing signals
+  ModArgs mod;      // modified scores (kMod kernels; the fp32 kernel reads softcap instead of k1 and cap2)
+  float softcap;
 };
 
 // Partition view built in shared memory by every CTA.
@@ -214,8 +216,13 @@ __device__ void build_plan(const KArgs& a, Plan& p, long long* pre, int* nlen, i
     } else {
       n = qp + 1 < kv ? qp + 1 : kv;
       if (a.window > 0 && qp - a.window + 1 > 0) lo = qp - a.window + 1;
-      if (lo >= n) {  // the window starts at or past the last cached key
-        if (blockIdx.x == 0) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+      if (a.mod.range) {  // the sequence's own keys, within those
+        const int2 rg = a.mod.range[b];
+        lo = max(lo, rg.x);
+        n = min(n, max(rg.y, 0));
+      }
+      if (lo >= n) {  // the window starts at or past the last cached key, or the range holds none
+        if (blockIdx.x == 0 && !a.mod.range) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
         n = 0;
         lo = 0;
       }
@@ -509,7 +516,7 @@ struct Bf16Cfg {
   static constexpr int kStatBytes = MT * 4 * 16 * 4;
   static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kQBytes) + kRedBytes +
                                   2 * kStatBytes + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 +
-                                  kStages * sizeof(TileMeta) + (2 * kStages + 1) * 8 + 1024;
+                                  kStages * sizeof(TileMeta) + (2 * kStages + 1) * 8 + kStages * 4 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -523,7 +530,8 @@ struct Bf16Cfg {
 //              (chunk-major, 16 rows each) instead of inside 64-row chunk planes
 constexpr int kContig = 0, kPaged2d = 1, kPaged3d = 2;
 
-template <int D, int MT, int kMode>
+// kMod: modified scores (a cap by tanh, a distance bias) on each 16-key slice's 8 scores per thread.
+template <int D, int MT, int kMode, bool kMod>
 __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv,
@@ -542,6 +550,8 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
   int* wlo = nlen + kMaxBatch;
   TileMeta* meta = reinterpret_cast<TileMeta*>(wlo + kMaxBatch);
   uint64_t* bars = reinterpret_cast<uint64_t*>(meta + C::kStages);
+  // kMod: position of each stage's first key minus the query's, written with the stage's descriptor
+  int* away = reinterpret_cast<int*>(bars + 2 * C::kStages + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -579,6 +589,7 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
     // chunks past the grid are handed out by the atomic ticket; with no more chunks than CTAs
     // (the automatic choice) every CTA has its one chunk and takes no ticket
     const bool dyn = plan.n_chunks > G;
+    int unit_away = 0;  // kMod: position of the unit's first key minus the query's
     // Writes the stage's descriptor and arms its full barrier for `kv_bytes` of K/V (+ the query
     // rows on a piece's first tile). Lane 0 only.
     auto arm = [&](const Piece& pc, int t, int slot, int nh, uint32_t kv_bytes, int nskip) -> uint32_t {
@@ -592,6 +603,13 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
       m.slot = slot;
       m.nh = nh;
       m.nskip = t == 0 ? nskip : 0;  // only a unit's first tile starts before the window
+      if constexpr (kMod) {
+        if (first) {
+          const int kv = a.kv_len ? a.kv_len[pc.b] : a.T_max;
+          unit_away = plan.wlo[pc.b] / a.gran * a.gran - (a.q_pos ? a.q_pos[pc.b] : kv - 1);
+        }
+        away[stage] = unit_away + t;
+      }
       meta[stage] = m;
       const uint32_t full = smem_u32(&bars[stage]);
       mbar_arrive_expect_tx(full, kv_bytes + (first ? C::kQBytes : 0));
@@ -782,10 +800,12 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
   uint32_t qf[NK][4];
   float acc[NN][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  float slope0 = 0.f, slope1 = 0.f;  // kMod: base-2 bias per key of distance of this thread's two rows
   while (true) {
     // ldmatrix / mma.sync below need the whole warp: leave together if the wait ran out
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[stage]), phase, a.err))) return;
     const TileMeta m = meta[stage];
+    const int key_away = kMod ? away[stage] : 0;
     if (m.flags & kEnd) {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars[C::kStages + stage]));
@@ -808,6 +828,12 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
       for (int n = 0; n < NN; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
+      if (kMod && a.mod.slopes) {
+        const float* sp = a.mod.slopes + m.g * a.r + m.hb * a.hpu;
+        const int r0 = mt * 16 + gid;
+        slope0 = r0 < m.nh ? sp[r0] * kLog2e : 0.f;
+        slope1 = r0 + 8 < m.nh ? sp[r0 + 8] * kLog2e : 0.f;
+      }
     }
     const int nvalid = m.nvalid;
     const int nskip = m.nskip;
@@ -828,6 +854,13 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
         }
       }
       // ---- mask, scale (base 2), online softmax update
+      float unit = sl2;  // base-2 score of one unit of sc
+      if constexpr (kMod) {
+        if (a.mod.cap2 > 0.f) {
+          tanh_scores<8>(&sc[0][0], a.mod.k1);
+          unit = a.mod.cap2;
+        }
+      }
       float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -835,8 +868,14 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           const int key = klo + 8 * j + 2 * tq + e;
           const bool vis = key < nvalid && key >= nskip;
-          sc[j][e] = vis ? sc[j][e] * sl2 : -INFINITY;
-          sc[j][2 + e] = vis ? sc[j][2 + e] * sl2 : -INFINITY;
+          float b0 = 0.f, b1 = 0.f;
+          if constexpr (kMod) {
+            const float far = fabsf((float)(key_away + key));
+            b0 = slope0 * far;
+            b1 = slope1 * far;
+          }
+          sc[j][e] = vis ? (kMod ? fmaf(sc[j][e], unit, -b0) : sc[j][e] * sl2) : -INFINITY;
+          sc[j][2 + e] = vis ? (kMod ? fmaf(sc[j][2 + e], unit, -b1) : sc[j][2 + e] * sl2) : -INFINITY;
           mx0 = fmaxf(mx0, sc[j][e]);
           mx1 = fmaxf(mx1, sc[j][2 + e]);
         }
@@ -1819,6 +1858,8 @@ __global__ void __launch_bounds__(32 * kF32Warps, 1) decode_fp32_kernel(KArgs a)
 #pragma unroll
         for (int e = 0; e < kF32MaxPerLane; ++e) accv[e] = 0.f;
         float m = -INFINITY, l = 0.f;
+        const float slope = a.mod.slopes ? a.mod.slopes[head] : 0.f;
+        const int qp = a.q_pos ? a.q_pos[pc.b] : (a.kv_len ? a.kv_len[pc.b] : a.T_max) - 1;
         for (int jr = max(pc.k0, jskip); jr < pc.k1; ++jr) {
           const int j = koff + jr;  // absolute key position
           const float* kj = kp + (long long)j * Dk;
@@ -1841,7 +1882,8 @@ __global__ void __launch_bounds__(32 * kF32Warps, 1) decode_fp32_kernel(KArgs a)
           }
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-          const float s = part * a.scale;
+          float t;
+          const float s = mod_score(part, a.scale, a.softcap, slope, (long long)qp - j, &t);
           const float m_new = fmaxf(m, s);
           const float alpha = expf(m - m_new);
           const float p = expf(s - m_new);
@@ -1925,10 +1967,10 @@ cudaError_t launch_dependent(void (*kern)(KParams...), int grid, int threads, si
   return e;
 }
 
-template <int D, int MT, int kMode>
+template <int D, int MT, int kMode, bool kMod>
 cudaError_t launch_bf16_typed(const KArgs& ka, const CUtensorMap* tm, int grid, cudaStream_t s) {
   using C = Bf16Cfg<D, MT>;
-  auto kern = decode_bf16_kernel<D, MT, kMode>;
+  auto kern = decode_bf16_kernel<D, MT, kMode, kMod>;
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -2013,6 +2055,8 @@ KArgs make_kargs(const DecodeArgs& a) {
   k.page_size = a.page_size;
   k.num_pages = a.num_pages;
   k.gran = a.block_table ? (a.page_size % kTile == 0 ? kTile : 16) : 1;
+  k.mod = mod_args(a.mod, a.scale);
+  k.softcap = a.mod.softcap;
   k.expire_wait = a.block_table || (a.mla && !a.mla_tc) ? 0 : a.expire_wait;
   return k;
 }
@@ -2042,28 +2086,34 @@ cudaError_t launch_decode_fp32(const DecodeArgs& a, cudaStream_t s) {
 }
 
 namespace dec {
-template <int kMode>
+template <int kMode, bool kMod>
 cudaError_t launch_bf16_dispatch(const KArgs& k, const CUtensorMap* tmaps, int grid, cudaStream_t s) {
   const bool two = k.hpu > 16;
   if (k.D == 128) {
-    return two ? launch_bf16_typed<128, 2, kMode>(k, tmaps, grid, s)
-               : launch_bf16_typed<128, 1, kMode>(k, tmaps, grid, s);
+    return two ? launch_bf16_typed<128, 2, kMode, kMod>(k, tmaps, grid, s)
+               : launch_bf16_typed<128, 1, kMode, kMod>(k, tmaps, grid, s);
   }
   if constexpr (kMode != kPaged3d) {
     if (k.D == 64) {
-      return two ? launch_bf16_typed<64, 2, kMode>(k, tmaps, grid, s)
-                 : launch_bf16_typed<64, 1, kMode>(k, tmaps, grid, s);
+      return two ? launch_bf16_typed<64, 2, kMode, kMod>(k, tmaps, grid, s)
+                 : launch_bf16_typed<64, 1, kMode, kMod>(k, tmaps, grid, s);
     }
   }
   return cudaErrorInvalidValue;
+}
+template <bool kMod>
+cudaError_t launch_bf16_modes(const DecodeArgs& a, const KArgs& k, const CUtensorMap* tmaps, cudaStream_t s) {
+  if (!a.block_table) return launch_bf16_dispatch<kContig, kMod>(k, tmaps, a.num_sms, s);
+  return a.paged_3d ? launch_bf16_dispatch<kPaged3d, kMod>(k, tmaps, a.num_sms, s)
+                    : launch_bf16_dispatch<kPaged2d, kMod>(k, tmaps, a.num_sms, s);
 }
 }  // namespace dec
 
 cudaError_t launch_decode_bf16(const DecodeArgs& a, const CUtensorMap* tmaps, cudaStream_t s) {
   const dec::KArgs k = dec::make_kargs(a);
-  if (!a.block_table) return dec::launch_bf16_dispatch<dec::kContig>(k, tmaps, a.num_sms, s);
-  return a.paged_3d ? dec::launch_bf16_dispatch<dec::kPaged3d>(k, tmaps, a.num_sms, s)
-                    : dec::launch_bf16_dispatch<dec::kPaged2d>(k, tmaps, a.num_sms, s);
+  // a key range alone only narrows the plan: the plain kernel serves it
+  return a.mod.softcap > 0.f || a.mod.slopes ? dec::launch_bf16_modes<true>(a, k, tmaps, s)
+                                             : dec::launch_bf16_modes<false>(a, k, tmaps, s);
 }
 
 cudaError_t launch_mla_bf16(const DecodeArgs& a, const CUtensorMap* tmaps, cudaStream_t s) {

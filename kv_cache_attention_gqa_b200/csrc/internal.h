@@ -10,6 +10,18 @@
 
 namespace gqa {
 
+// Modified scores as a call passes them (gqa_score_mod); off when nothing is set.
+struct ScoreMod {
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  const int32_t* range = nullptr;  // (B, S_q, 2), decode (B, 2)
+  bool on() const { return softcap > 0.f || slopes || range; }
+};
+struct ModArgs;
+ModArgs mod_args(const ScoreMod& m, float scale);  // without the hull
+// per (sequence, block of `rows` query rows): ModArgs::hull; n_blocks = ceil(S_q / rows)
+cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks, cudaStream_t s);
+
 struct AppendArgs {
   void* k_cache;
   void* v_cache;
@@ -118,6 +130,8 @@ struct PrefillArgs {
   int window;  // 0: none; W > 0 (causal only): row at position p sees keys p - W < j <= p
   int expire_wait = 0;  // test hook (gqa_debug_expire_waits): one bounded wait runs out
   unsigned* err;
+  ScoreMod mod;
+  void* workspace = nullptr;  // bf16 with key ranges: the tiles' hulls
 };
 // fp32 check mode (scalar FFMA)
 cudaError_t launch_prefill_fp32(const PrefillArgs& a, cudaStream_t s);
@@ -147,6 +161,8 @@ struct BackwardArgs {
   float* drow;  // workspace: (B*h_q*S_q) rowsum(dO * O)
   int* ticket;  // workspace: the bf16 kernel's work-item counter (reset by its row-term kernel)
   unsigned* err;
+  ScoreMod mod;
+  void* hull = nullptr;  // bf16 with key ranges: the hulls of the dQ tiles, then of 64-row query blocks
 };
 // bf16 tcgen05 path. tmaps: [0] Q, [1] dO as 3-D views (d_h, S_q, B*h_q) with box (64, 64, 1);
 // [2] K, [3] V as 2-D views (d_h, B*h_kv*T_max) with box (64, 128); [4] Q, [5] dO as 3-D views
@@ -154,6 +170,8 @@ struct BackwardArgs {
 cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps, int num_sms,
                                  cudaStream_t s);
 cudaError_t launch_backward_fp32(const BackwardArgs& a, cudaStream_t s);
+size_t backward_hull_bytes(int B, int h_q, int h_kv, int S_q);  // BackwardArgs::hull
+size_t prefill_hull_bytes(int B, int h_q, int h_kv, int S_q);   // PrefillArgs::workspace
 
 struct DecodeArgs {
   const void* q;
@@ -187,6 +205,7 @@ struct DecodeArgs {
   // chunk on two CTAs (one per half of the 512 value columns)
   int mla_tc = 0;
   int expire_wait = 0;  // test hook (gqa_debug_expire_waits), contiguous bf16 decode only
+  ScoreMod mod;         // not for MLA
 };
 
 // The host-side argument checks of gqa_decode (contiguous: cache_rows = B * h_kv * T_max), in

@@ -48,6 +48,10 @@
 // Registers: the launch gives 168 per thread (3 warps of 168 fill a sub-partition's 16,384); the
 // first warpgroup gives back down to 72 and each softmax warpgroup takes 216 (72 + 216 + 216 =
 // 3 x 168), which holds a thread's 128 scores without spilling.
+// kMod kernels (modified scores): each thread caps its 128 scores by tanh (a polynomial while they are small
+// against the cap, so that the exponential unit keeps to the softmax; see tanh_scores) and adds the distance bias
+// before the maximum, and a row's key range joins its two 32-bit bounds. A tile's blocks run from the least to the
+// largest key its rows see, which a small kernel in front works out per tile (row_hull).
 // TMEM columns: tile t holds S_t at [256 t, 256 t + 128) and O_t at [256 t + 128, 256 t + 128 + D).
 
 #include <math.h>
@@ -109,6 +113,7 @@ struct PArgs {
   int window;  // 0: none; W > 0: row at position p also needs key j > p - W (causal only)
   int expire_wait;  // test hook: CTA 0's producer first waits on a barrier that nothing signals
   unsigned* err;
+  ModArgs mod;  // kMod kernels only; mod.hull has an entry per sequence and tile of P positions
 };
 
 // barrier indices inside the barrier block (derived from the ring depths, so they never overlap)
@@ -168,6 +173,7 @@ struct Work {
   int nb[kTiles];    // blocks chain t visits: pair mode j0 .. j0 + nb[t] - 1 (nb[0] <= nb[1]);
                      // split mode j0 + t, j0 + t + 2, ... (nb[0] >= nb[1])
   int nbmax;         // K/V blocks the item loads
+  int lo_key, hi_key;  // kMod: keys [lo_key, hi_key) that some row of the item sees
   bool valid;
   // nb[t] for a chain index known only at run time. (A run-time index into a struct's array puts
   // the struct in local memory, which the shared-memory carve-out leaves almost no L1 for: the
@@ -182,6 +188,7 @@ struct Work {
 };
 
 // Item idx: items are numbered heaviest (latest positions) first.
+template <bool kMod>
 __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
   Work w;
   const int per = a.B * a.h_kv * a.hblocks;
@@ -204,8 +211,41 @@ __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
   w.nbmax = 0;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) w.nb[t] = 0;
+  w.lo_key = 0;
+  w.hi_key = w.kv;
   if (!w.valid) return w;
-  if (a.causal) {
+  if constexpr (kMod) {
+    // the keys each tile's rows see, by their ranges, positions and window, and the blocks that hold them
+    int lo[kTiles], hi[kTiles];
+    w.lo_key = w.kv;
+    w.hi_key = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      lo[t] = hi[t] = 0;
+      if (t >= w.nq) continue;
+      const int row0 = w.q0 + t * a.P;
+      long long l = 0, h = w.kv;
+      if (a.causal) {
+        const long long last = (long long)w.qs + min(row0 + a.P, a.S_q);  // one past the latest position
+        if (last < h) h = last;
+        if (a.window > 0 && (long long)w.qs + row0 - a.window + 1 > l) l = (long long)w.qs + row0 - a.window + 1;
+      }
+      if (a.mod.hull) {
+        const int4 hl = a.mod.hull[(long long)w.b * a.n_qt + (w.split ? pr : pr * kTiles + t)];
+        if (hl.x > l) l = hl.x;
+        if (hl.y < h) h = hl.y;
+      }
+      if (l >= h) continue;
+      lo[t] = (int)l;
+      hi[t] = (int)h;
+      w.lo_key = min(w.lo_key, lo[t]);
+      w.hi_key = max(w.hi_key, hi[t]);
+    }
+    if (w.hi_key == 0) w.lo_key = 0;
+    w.j0 = w.lo_key / kBN;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) w.nb[t] = hi[t] > 0 ? (hi[t] + kBN - 1) / kBN - w.j0 : 0;
+  } else if (a.causal) {
     if (a.window > 0) {
       // blocks wholly below the earliest row's window are skipped [第三章 §3.7: each query reads
       // only its local window]
@@ -226,7 +266,7 @@ __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
     for (int t = 0; t < kTiles; ++t)
       if (t < w.nq) w.nb[t] = (w.kv + kBN - 1) / kBN;
   }
-  w.nbmax = w.nq == 2 ? w.nb[1] : w.nb[0];
+  w.nbmax = kMod ? max(w.nb[0], w.nb[1]) : w.nq == 2 ? w.nb[1] : w.nb[0];
   if (w.split) {  // the tile's blocks alternate between the chains
     w.nb[0] = (w.nbmax + 1) / 2;
     w.nb[1] = w.nbmax / 2;
@@ -289,7 +329,7 @@ __device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) 
 // xm: 512 floats of shared memory for the split-mode merge (the unused second Q tile); xabort: a
 // word that a split-mode chain sets before the merge when it gave up, read by both chains after
 // the merge's first barrier, so that both take the same path through the barriers.
-template <int D, bool kWin, bool kSplit>
+template <int D, bool kWin, bool kSplit, bool kMod>
 __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int lane, uint32_t tmem,
                                              uint32_t sV, uint64_t* bars, float* xm,
                                              volatile int* xabort, volatile int* abort) {
@@ -299,7 +339,9 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
   const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
   const uint32_t colS = C::colS(t), colO = C::colO(t);
   const int h = row / a.P, p = row - h * a.P;
-  const float c = a.scale_log2;
+  // scores are in units of 1 / c (base 2): raw products, or (kMod with a cap or a bias) base-2 scores
+  const bool transform = kMod && (a.mod.cap2 > 0.f || a.mod.slopes);
+  const float c = transform ? 1.f : a.scale_log2;
   const int win = kWin ? a.window : 0;
   // running counts over the CTA's items (see Seq): K/V blocks loaded, this chain's blocks, rounds
   // of the other chain this chain's turn waits count (its arrivals), and this chain's arrivals
@@ -310,7 +352,7 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
   for (int it = 0; !kSplit || it < 1; ++it) {  // split mode: one item per CTA
     const long long item = item_of(it);
     if (item >= a.n_items) break;
-    const Work w = make_work(a, (int)item);
+    const Work w = make_work<kMod>(a, (int)item);
     const int J0 = cJ, I0 = cI, T0 = cT, A0 = cA;  // counts before this item
     cJ += w.nbmax;
     if (t < w.nt) cI += w.nbt(t);
@@ -325,14 +367,29 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
     const long long pos = (long long)w.qs + qi;
     // last key this row may see (length and causal limits in one 32-bit bound for the mask loop)
     const long long kl = a.causal && pos < w.kv - 1 ? pos : (long long)w.kv - 1;
-    const int key_last = (int)kl;
+    int key_last = (int)kl;
     const long long pos_min = (long long)w.qs + qt0;                        // smallest in the tile
     const long long pos_max = (long long)w.qs + min(qt0 + a.P, a.S_q) - 1;  // largest in the tile
     const long long item_pos_min = (long long)w.qs + w.q0;                  // smallest in the item
     const int nb = w.nbt(t);
     // last key below this row's window, clamped to the int range (keys are ints)
     const long long wl = pos - win;
-    const int win_last = kWin ? (int)(wl < -1 ? -1 : (wl > 0x7fffffffLL ? 0x7fffffffLL : wl)) : -1;
+    int win_last = kWin ? (int)(wl < -1 ? -1 : (wl > 0x7fffffffLL ? 0x7fffffffLL : wl)) : -1;
+    float slope2 = 0.f;  // bias per key of distance, base 2
+    if constexpr (kMod) {
+      if (a.window > 0) {
+        const long long ml = pos - a.window;
+        win_last = (int)(ml < -1 ? -1 : (ml > 0x7fffffffLL ? 0x7fffffffLL : ml));
+      }
+      if (store_row) {
+        if (a.mod.range) {
+          const int2 rg = a.mod.range[(long long)w.b * a.S_q + qi];
+          win_last = max(win_last, rg.x > 0 ? rg.x - 1 : -1);
+          key_last = min(key_last, rg.y - 1);
+        }
+        if (a.mod.slopes) slope2 = a.mod.slopes[w.g * a.r + w.hb * a.H + h] * kLog2e;
+      }
+    }
     const long long orow = ((long long)w.b * a.h_q + w.g * a.r + w.hb * a.H + h) * a.S_q + qi;
     __nv_bfloat16* const orow_ptr = reinterpret_cast<__nv_bfloat16*>(a.o) + orow * D;
 
@@ -369,13 +426,34 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       for (int q = 0; q < 4; ++q) tc::ld32f(lane_addr + colS + q * 32, sr + q * 32);
       tc::wait_ld();
       const int key0 = (w.j0 + j) * kBN;  // first key of the block
-      const bool need_mask = (a.causal && (long long)key0 + kBN - 1 > pos_min) || key0 + kBN > w.kv ||
-                             (kWin && (long long)key0 <= pos_max - win);
+      bool need_mask = (a.causal && (long long)key0 + kBN - 1 > pos_min) || key0 + kBN > w.kv ||
+                       (kWin && (long long)key0 <= pos_max - win);
+      if constexpr (kMod) {
+        need_mask = __any_sync(0xffffffffu, store_row && (key0 <= win_last || key0 + kBN - 1 > key_last));
+        if (a.mod.cap2 > 0.f) {
+          tanh_scores<kBN>(sr, a.mod.k1);
+          const float2 m2 = make_float2(a.mod.cap2, a.mod.cap2);
+#pragma unroll
+          for (int k = 0; k < kBN; k += 2) {
+            const float2 y = pair_mul(make_float2(sr[k], sr[k + 1]), m2);
+            sr[k] = y.x;
+            sr[k + 1] = y.y;
+          }
+        } else if (transform) {
+#pragma unroll
+          for (int k = 0; k < kBN; ++k) sr[k] *= a.scale_log2;
+        }
+        if (a.mod.slopes) {
+          const float away = (float)(key0 - pos);  // the first key's distance; exact below 2^24
+#pragma unroll
+          for (int k = 0; k < kBN; ++k) sr[k] = fmaf(-slope2, fabsf(away + (float)k), sr[k]);
+        }
+      }
       if (need_mask) {
 #pragma unroll
         for (int k = 0; k < kBN; ++k) {
           const int key = key0 + k;
-          const bool vis = key <= key_last && (!kWin || key > win_last);
+          const bool vis = key <= key_last && (!(kWin || kMod) || key > win_last);
           sr[k] = vis ? sr[k] : -INFINITY;
         }
       }
@@ -472,14 +550,16 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       // both tiles zero them (the two chains' MMAs are not ordered); a second write stores the
       // same zeros.
       const int bkey0 = (w.j0 + j) * kBN;
-      const bool zero_tail = bkey0 + kBN > w.kv;
-      const bool zero_head = kWin && j == 0 && (long long)bkey0 < item_pos_min - win + 1;
+      const bool zero_tail = bkey0 + kBN > (kMod ? w.hi_key : w.kv);
+      const bool zero_head = kMod ? bkey0 < w.lo_key : kWin && j == 0 && (long long)bkey0 < item_pos_min - win + 1;
       if (ok && (zero_tail || zero_head)) {
         const int jg = J0 + j;  // block count over the CTA's items
         const int vs = jg % kVStages;
         if (wait_bar(bar(kBarVFull + vs), (uint32_t)((jg / kVStages) & 1), abort, a.err)) {
           const long long key = (long long)bkey0 + row;  // thread `row` owns V row `row` of the block
-          if (row < kBN && ((zero_tail && key >= w.kv) || (zero_head && key <= item_pos_min - win))) {
+          const bool none = kMod ? key >= w.hi_key || key < w.lo_key
+                                 : (zero_tail && key >= w.kv) || (zero_head && key <= item_pos_min - win);
+          if (row < kBN && none) {
 #pragma unroll
             for (int ch = 0; ch < C::kNch; ++ch) {
 #pragma unroll
@@ -515,8 +595,8 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       // it still takes part in the warp's TMEM loads, and writes zeros. The next item's first
       // O += P V, which overwrites O, waits for this warpgroup's P of that item, so it comes
       // after these loads.
-      const bool empty = kWin && l == 0.f;
-      if (empty && store_row) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+      const bool empty = (kWin || kMod) && l == 0.f;
+      if (empty && store_row && !(kMod && a.mod.range)) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
       const float inv = empty ? 0.f : 1.f / l;
       uint4* out = reinterpret_cast<uint4*>(orow_ptr);
 #pragma unroll
@@ -554,7 +634,7 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       const float m0 = xm[row], l0 = xm[128 + row], m1 = xm[256 + row], l1 = xm[384 + row];
       const float M = fmaxf(m0, m1);
       const bool empty = M == -INFINITY;  // no visible key in either chain (sliding window)
-      if (empty && store_row && t == 0) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+      if (empty && store_row && t == 0 && !(kMod && a.mod.range)) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
       const float f0 = empty || w.nb[0] == 0 ? 0.f : fast_exp2(m0 - M);
       const float f1 = empty || w.nb[1] == 0 ? 0.f : fast_exp2(m1 - M);
       const float L = l0 * f0 + l1 * f1;
@@ -601,7 +681,7 @@ using tc::elect_one;
 // are built once: the start address sits in the low 14 bits (address >> 4, below 2^14 for any
 // shared-memory address), so the descriptor of base + offset is the base's descriptor plus
 // offset >> 4.
-template <int D, bool kSplit>
+template <int D, bool kSplit, bool kMod>
 __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, uint32_t sQ,
                                          uint32_t sK, uint32_t sV, uint64_t* bars,
                                          volatile int* abort) {
@@ -653,7 +733,7 @@ __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, u
   for (int it = 0; ok && (!kSplit || it < 1); ++it) {  // split mode: one item per CTA
     const long long item = item_of(it);
     if (item >= a.n_items) break;
-    const Work w = make_work(a, (int)item);
+    const Work w = make_work<kMod>(a, (int)item);
     const Seq s0 = sq;
     advance(sq, w);
     const int nb = t < w.nt ? w.nbt(t) : 0;
@@ -709,7 +789,7 @@ __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, u
   wait_bar(bar(kBarDone + t), 0, &no_abort, a.err);
 }
 
-template <int D, bool kWin, bool kSplit>
+template <int D, bool kWin, bool kSplit, bool kMod>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmq,
                         const __grid_constant__ CUtensorMap tmk,
@@ -791,12 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; ok && (!kSplit || it < 1); ++it) {  // split mode: one item per CTA
       const long long item = item_of(it);
       if (item >= a.n_items) break;
-      const Work w = make_work(a, (int)item);
+      const Work w = make_work<kMod>(a, (int)item);
       const Seq s0 = sq;
       advance(sq, w);
       if (!w.valid) set_device_error(a.err, w.kv < 1 || w.kv > a.T_max ? GQA_DEVERR_KV_LEN
                                                                         : GQA_DEVERR_POSITION);
-      else if (w.nb[0] == 0) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+      else if (w.nb[0] == 0 && !(kMod && a.mod.range)) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
       // the Q rows of every chain that runs (split mode: the one tile both chains read)
       const int zq = w.b * a.h_q + w.g * a.r + w.hb * a.H;  // first head of the block
 #pragma unroll
@@ -854,13 +934,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nv > s) wait_bar(bar(kBarVFull + s), (uint32_t)(((nv - 1 - s) / kVStages) & 1), &no_abort, a.err);
     } else if (warp == 1 || warp == 2) {
       // ------------------------------ MMA issuer of tile t ----------------------------------
-      mma_role<D, kSplit>(a, warp - 1, tmem, sQ, sK, sV, bars, abort);
+      mma_role<D, kSplit, kMod>(a, warp - 1, tmem, sQ, sK, sV, bars, abort);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = (warp - kSoftmaxWarp0) >> 2;
     float* xm = reinterpret_cast<float*>(smem + C::kOffQ + C::kQBytes);  // second Q tile (split mode)
-    softmax_role<D, kWin, kSplit>(a, t, warp & 3, lane, tmem, sV, bars, xm, xabort, abort);
+    softmax_role<D, kWin, kSplit, kMod>(a, t, warp & 3, lane, tmem, sV, bars, xm, xabort, abort);
   }
 
   tc::fence_before_sync();
@@ -871,9 +951,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kWin, bool kSplit>
+template <int D, bool kWin, bool kSplit, bool kMod = false>
 cudaError_t launch_typed(const PArgs& p, const CUtensorMap* tmaps, long long ctas, cudaStream_t s) {
-  auto kern = prefill_bf16_kernel<D, kWin, kSplit>;
+  auto kern = prefill_bf16_kernel<D, kWin, kSplit, kMod>;
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -929,6 +1009,20 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
   // fewer; split mode (chosen when the items barely fill the SMs): one CTA per item
   const long long ctas = p.split || items < num_sms ? items : num_sms;
   const bool win = a.window > 0;
+  if (a.mod.on()) {
+    p.mod = mod_args(a.mod, a.scale);
+    if (a.mod.range) {
+      int4* hull = reinterpret_cast<int4*>(a.workspace);
+      const cudaError_t e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, n_qt, s);
+      if (e != cudaSuccess) return e;
+      p.mod.hull = hull;
+    }
+    if (a.d_h == 128) return p.split ? pf::launch_typed<128, false, true, true>(p, tmaps, ctas, s)
+                                     : pf::launch_typed<128, false, false, true>(p, tmaps, ctas, s);
+    if (a.d_h == 64) return p.split ? pf::launch_typed<64, false, true, true>(p, tmaps, ctas, s)
+                                    : pf::launch_typed<64, false, false, true>(p, tmaps, ctas, s);
+    return cudaErrorInvalidValue;
+  }
   if (a.d_h == 128) {
     if (p.split) return win ? pf::launch_typed<128, true, true>(p, tmaps, ctas, s)
                             : pf::launch_typed<128, false, true>(p, tmaps, ctas, s);
@@ -942,6 +1036,11 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
                : pf::launch_typed<64, false, false>(p, tmaps, ctas, s);
   }
   return cudaErrorInvalidValue;
+}
+
+size_t prefill_hull_bytes(int B, int h_q, int h_kv, int S_q) {
+  const int P = pf::kBM / prefill_heads_per_tile(h_q, h_kv);
+  return (size_t)((S_q + P - 1) / P) * B * sizeof(int4);
 }
 
 int prefill_heads_per_tile(int h_q, int h_kv) {

@@ -32,6 +32,7 @@ from .paged import gather_pages, paged_append_ref, paged_decode_ref
 from .backward import attention_backward_ref, softmax_backward_rowterm
 from .mla import mla_decode_ref, mla_explicit_ref
 from .rope import rope_ref
+from .score_mod import modified_attention_ref
 from .kv_weights import kv_weights_ref
 from .kv_evict import kv_evict_ref
 from . import ledgers
@@ -54,6 +55,7 @@ __all__ = [
     "mla_decode_ref",
     "mla_explicit_ref",
     "rope_ref",
+    "modified_attention_ref",
     "kv_weights_ref",
     "kv_evict_ref",
     "ledgers",
