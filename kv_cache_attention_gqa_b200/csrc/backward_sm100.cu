@@ -81,6 +81,11 @@ struct BArgs {
   const int4* hull64;       // kMod with ranges: of the 64-row query blocks (dkdv)
 };
 
+template <int N>
+struct Int {  // a number as a type, for loops that are compiled once per case
+  static constexpr int value = N;
+};
+
 // Bounded mbarrier wait shared by all roles: gives up after 2 s (or when another thread of the
 // CTA gave up), records GQA_DEVERR_TIMEOUT and returns false.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort,
@@ -501,34 +506,73 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
       if (cap) tanh_scores<32>(sf, a.mod.k1);
       const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
       // kMod: bias per key of distance (base 2) of this block's head, and the distance of its first row
-      const float slope2 = kMod && a.mod.slopes ? a.mod.slopes[head_of(it)] * kLog2e : 0.f;
+      // (columns on from pos0; key at or before every row, as under the causal mask: the bias falls along them)
+      const bool bias = kMod && a.mod.slopes;
+      const float slope2 = bias ? a.mod.slopes[head_of(it)] * kLog2e : 0.f;
       const float away = (float)(pos0 - key);
-#pragma unroll
-      for (int x = 0; x < 32; x += 2) {
-        const float2 nl = *reinterpret_cast<const float2*>(sl + x);          // -lse2 of the two rows
-        const float2 nd = *reinterpret_cast<const float2*>(sl + kKvBQ + x);  // -D of the two rows
-        float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
-        if (kMod && a.mod.slopes) {
-          arg.x = fmaf(-slope2, fabsf(away + (float)x), arg.x);
-          arg.y = fmaf(-slope2, fabsf(away + (float)(x + 1)), arg.y);
-        }
-        float2 p = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
-        float2 ds = mul2(p, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd));
-        if (cap) {
-          const float2 t = make_float2(sf[x], sf[x + 1]);
-          ds = mul2(ds, fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
-        }
-        if (kMod && ranged) {
-          const int2 lo = *reinterpret_cast<const int2*>(rl + x), hi = *reinterpret_cast<const int2*>(rl + kKvBQ + x);
-          if (key < lo.x || key >= hi.x) p.x = ds.x = 0.f;
-          if (key < lo.y || key >= hi.y) p.y = ds.y = 0.f;
-        }
+      const bool rows_after = a.causal || (long long)k0 + kBK - 1 <= pos0, rows_before = pos0 + 31 <= k0;
+      const bool one = rows_after || rows_before;
+      const float step = rows_after ? -slope2 : slope2, from = step * away;
+      // kMod: which of the 32 columns see this key, as bits
+      uint32_t sees = 0xffffffffu;
+      if constexpr (kMod) {
         if (need_mask) {
-          if (x < c_lo || x >= c_hi) p.x = ds.x = 0.f;
-          if (x + 1 < c_lo || x + 1 >= c_hi) p.y = ds.y = 0.f;
+          const uint32_t below = c_hi >= 32 ? 0xffffffffu : (1u << c_hi) - 1u;
+          sees = c_lo >= 32 ? 0u : below & (0xffffffffu << c_lo);
         }
-        pp[x / 2] = pack_bf16x2(p.x, p.y);
-        pd[x / 2] = pack_bf16x2(ds.x, ds.y);
+        if (ranged) {
+          uint32_t in = 0;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const int4 lo = *reinterpret_cast<const int4*>(rl + x), hi = *reinterpret_cast<const int4*>(rl + kKvBQ + x);
+            in |= (key >= lo.x && key < hi.x ? 1u : 0u) << x | (key >= lo.y && key < hi.y ? 2u : 0u) << x |
+                  (key >= lo.z && key < hi.z ? 4u : 0u) << x | (key >= lo.w && key < hi.w ? 8u : 0u) << x;
+          }
+          sees &= in;
+        }
+      }
+      // A loop per case, so that none carries another's work. kBias: 0 none, 1 linear along the columns, 2 by
+      // distance; kMask: some column does not see some key.
+      auto columns = [&](auto kBias, auto kMask) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float2 nl = *reinterpret_cast<const float2*>(sl + x);          // -lse2 of the two rows
+          const float2 nd = *reinterpret_cast<const float2*>(sl + kKvBQ + x);  // -D of the two rows
+          float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
+          if constexpr (kBias.value == 1) {
+            arg.x += fmaf(step, (float)x, from);
+            arg.y += fmaf(step, (float)(x + 1), from);
+          } else if constexpr (kBias.value == 2) {
+            arg.x = fmaf(-slope2, fabsf(away + (float)x), arg.x);
+            arg.y = fmaf(-slope2, fabsf(away + (float)(x + 1)), arg.y);
+          }
+          float2 p = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
+          float2 ds = mul2(p, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd));
+          if (cap) {
+            const float2 t = make_float2(sf[x], sf[x + 1]);
+            ds = mul2(ds, fma2(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f)));
+          }
+          if constexpr (kMod && kMask.value) {
+            if (!(sees >> x & 1u)) p.x = ds.x = 0.f;
+            if (!(sees >> (x + 1) & 1u)) p.y = ds.y = 0.f;
+          } else if (!kMod && need_mask) {
+            if (x < c_lo || x >= c_hi) p.x = ds.x = 0.f;
+            if (x + 1 < c_lo || x + 1 >= c_hi) p.y = ds.y = 0.f;
+          }
+          pp[x / 2] = pack_bf16x2(p.x, p.y);
+          pd[x / 2] = pack_bf16x2(ds.x, ds.y);
+        }
+      };
+      if constexpr (!kMod) {
+        columns(Int<0>(), Int<0>());
+      } else if (need_mask || ranged) {
+        if (!bias) columns(Int<0>(), Int<1>());
+        else if (one) columns(Int<1>(), Int<1>());
+        else columns(Int<2>(), Int<1>());
+      } else {
+        if (!bias) columns(Int<0>(), Int<0>());
+        else if (one) columns(Int<1>(), Int<0>());
+        else columns(Int<2>(), Int<0>());
       }
       tc::st16(lane_addr + 64 * bf + 32 * half, pp);        // P^T over this half's first columns
       tc::st16(lane_addr + 128 + 64 * bf + 32 * half, pd);  // dS^T likewise in dP^T
@@ -951,7 +995,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         if (!ok) break;
         const int blk0 = (t.j0 + j) * kQBK;
         const int key0 = blk0 + half * 32;  // first key of this half
-        const bool need_mask = kMod ? store_row && (key0 < k_first || key0 + 31 > k_last)
+        const bool need_mask = kMod ? __any_sync(0xffffffffu, store_row && (key0 < k_first || key0 + 31 > k_last)) != 0
                                     : (a.causal && (long long)key0 + 31 > t.pos_min) || key0 + 32 > t.kv ||
                                           (a.window > 0 && (long long)key0 <= t.pos_max - a.window);
         tc::fence_after_sync();
@@ -965,25 +1009,46 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         if (cap) tanh_scores<32>(sf, a.mod.k1);
         const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
         const float2 nl = make_float2(-lse2, -lse2), nd2 = make_float2(-dr, -dr);
+        // distances key - pos of this half's keys: linear in the key on one side of the tile's rows
+        const bool bias = kMod && a.mod.slopes;
         const float away = (float)(key0 - pos);
+        const bool before = a.causal || key0 + 31 <= t.pos_min, after = key0 >= t.pos_max;
+        const bool one = before || after;
+        const float step = before ? slope2 : -slope2, from = step * away - lse2;
+        auto columns = [&](auto kBias, auto kMask) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nl);
-          if (kMod && a.mod.slopes) {
-            arg.x = fmaf(-slope2, fabsf(away + (float)x), arg.x);
-            arg.y = fmaf(-slope2, fabsf(away + (float)(x + 1)), arg.y);
+          for (int x = 0; x < 32; x += 2) {
+            float2 nb = nl;
+            if constexpr (kBias.value == 1) {
+              nb = make_float2(fmaf(step, (float)x, from), fmaf(step, (float)(x + 1), from));
+            } else if constexpr (kBias.value == 2) {
+              nb = make_float2(fmaf(-slope2, fabsf(away + (float)x), -lse2),
+                               fmaf(-slope2, fabsf(away + (float)(x + 1)), -lse2));
+            }
+            const float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nb);
+            const float2 pr = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
+            float2 ds = mul2(pr, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd2));
+            if (cap) {
+              const float2 tt = make_float2(sf[x], sf[x + 1]);
+              ds = mul2(ds, fma2(make_float2(-tt.x, -tt.y), tt, make_float2(1.f, 1.f)));
+            }
+            if (kMod ? kMask.value != 0 : need_mask) {
+              if (key0 + x < k_first || key0 + x > k_last) ds.x = 0.f;
+              if (key0 + x + 1 < k_first || key0 + x + 1 > k_last) ds.y = 0.f;
+            }
+            pd[x / 2] = pack_bf16x2(ds.x, ds.y);
           }
-          const float2 pr = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
-          float2 ds = mul2(pr, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd2));
-          if (cap) {
-            const float2 tt = make_float2(sf[x], sf[x + 1]);
-            ds = mul2(ds, fma2(make_float2(-tt.x, -tt.y), tt, make_float2(1.f, 1.f)));
-          }
-          if (need_mask) {
-            if (key0 + x < k_first || key0 + x > k_last) ds.x = 0.f;
-            if (key0 + x + 1 < k_first || key0 + x + 1 > k_last) ds.y = 0.f;
-          }
-          pd[x / 2] = pack_bf16x2(ds.x, ds.y);
+        };
+        if constexpr (!kMod) {
+          columns(Int<0>(), Int<0>());
+        } else if (need_mask) {
+          if (!bias) columns(Int<0>(), Int<1>());
+          else if (one) columns(Int<1>(), Int<1>());
+          else columns(Int<2>(), Int<1>());
+        } else {
+          if (!bias) columns(Int<0>(), Int<0>());
+          else if (one) columns(Int<1>(), Int<0>());
+          else columns(Int<2>(), Int<0>());
         }
         tc::st16(lane_addr + 64 * bf + 32 * half, pd);  // dS over this half's first columns of S
         // K rows no row of the tile may see (past kv_len: last block; below every row's window:

@@ -339,9 +339,10 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
   const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
   const uint32_t colS = C::colS(t), colO = C::colO(t);
   const int h = row / a.P, p = row - h * a.P;
-  // scores are in units of 1 / c (base 2): raw products, or (kMod with a cap or a bias) base-2 scores
-  const bool transform = kMod && (a.mod.cap2 > 0.f || a.mod.slopes);
-  const float c = transform ? 1.f : a.scale_log2;
+  // base-2 score = sr c: sr holds raw products, kMod: their tanh under a cap, or with a bias the score itself
+  const bool cap = kMod && a.mod.cap2 > 0.f, bias = kMod && a.mod.slopes;
+  const float unit = cap ? a.mod.cap2 : a.scale_log2;
+  const float c = bias ? 1.f : unit;
   const int win = kWin ? a.window : 0;
   // running counts over the CTA's items (see Seq): K/V blocks loaded, this chain's blocks, rounds
   // of the other chain this chain's turn waits count (its arrivals), and this chain's arrivals
@@ -430,23 +431,21 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
                        (kWin && (long long)key0 <= pos_max - win);
       if constexpr (kMod) {
         need_mask = __any_sync(0xffffffffu, store_row && (key0 <= win_last || key0 + kBN - 1 > key_last));
-        if (a.mod.cap2 > 0.f) {
-          tanh_scores<kBN>(sr, a.mod.k1);
-          const float2 m2 = make_float2(a.mod.cap2, a.mod.cap2);
+        if (cap) tanh_scores<kBN>(sr, a.mod.k1);
+        if (bias) {
+          // distances key - pos from the block's first key on (exact below 2^24); under the causal mask, and where
+          // the block lies on one side of every row, the bias is linear along the block
+          const float away = (float)(key0 - pos);
+          const bool before = a.causal || __all_sync(0xffffffffu, !store_row || key0 + kBN - 1 <= pos);
+          const bool after = __all_sync(0xffffffffu, !store_row || key0 >= pos);
+          const float step = before ? slope2 : -slope2, from = step * away;
+          if (before || after) {
 #pragma unroll
-          for (int k = 0; k < kBN; k += 2) {
-            const float2 y = pair_mul(make_float2(sr[k], sr[k + 1]), m2);
-            sr[k] = y.x;
-            sr[k + 1] = y.y;
+            for (int k = 0; k < kBN; ++k) sr[k] = fmaf(sr[k], unit, fmaf(step, (float)k, from));
+          } else {
+#pragma unroll
+            for (int k = 0; k < kBN; ++k) sr[k] = fmaf(sr[k], unit, -slope2 * fabsf(away + (float)k));
           }
-        } else if (transform) {
-#pragma unroll
-          for (int k = 0; k < kBN; ++k) sr[k] *= a.scale_log2;
-        }
-        if (a.mod.slopes) {
-          const float away = (float)(key0 - pos);  // the first key's distance; exact below 2^24
-#pragma unroll
-          for (int k = 0; k < kBN; ++k) sr[k] = fmaf(-slope2, fabsf(away + (float)k), sr[k]);
         }
       }
       if (need_mask) {
