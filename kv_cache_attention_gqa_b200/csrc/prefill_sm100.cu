@@ -56,6 +56,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -97,6 +99,10 @@ struct Cfg {
   static constexpr uint32_t colS(int t) { return (uint32_t)(256 * t); }
   static constexpr uint32_t colO(int t) { return (uint32_t)(256 * t + 128); }
 };
+
+// kMod: kernels with modified scores (0: plain). A cap and a bias are compiled in, not branched on: the blocks'
+// register-resident loops then hold one case each.
+constexpr int kModOn = 1, kModCap = 2, kModBias = 4;
 
 struct PArgs {
   void* o;
@@ -188,7 +194,7 @@ struct Work {
 };
 
 // Item idx: items are numbered heaviest (latest positions) first.
-template <bool kMod>
+template <int kMod>
 __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
   Work w;
   const int per = a.B * a.h_kv * a.hblocks;
@@ -329,7 +335,7 @@ __device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) 
 // xm: 512 floats of shared memory for the split-mode merge (the unused second Q tile); xabort: a
 // word that a split-mode chain sets before the merge when it gave up, read by both chains after
 // the merge's first barrier, so that both take the same path through the barriers.
-template <int D, bool kWin, bool kSplit, bool kMod>
+template <int D, bool kWin, bool kSplit, int kMod>
 __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int lane, uint32_t tmem,
                                              uint32_t sV, uint64_t* bars, float* xm,
                                              volatile int* xabort, volatile int* abort) {
@@ -340,7 +346,7 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
   const uint32_t colS = C::colS(t), colO = C::colO(t);
   const int h = row / a.P, p = row - h * a.P;
   // base-2 score = sr c: sr holds raw products, kMod: their tanh under a cap, or with a bias the score itself
-  const bool cap = kMod && a.mod.cap2 > 0.f, bias = kMod && a.mod.slopes;
+  constexpr bool cap = (kMod & kModCap) != 0, bias = (kMod & kModBias) != 0;
   const float unit = cap ? a.mod.cap2 : a.scale_log2;
   const float c = bias ? 1.f : unit;
   const int win = kWin ? a.window : 0;
@@ -388,7 +394,7 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
           win_last = max(win_last, rg.x > 0 ? rg.x - 1 : -1);
           key_last = min(key_last, rg.y - 1);
         }
-        if (a.mod.slopes) slope2 = a.mod.slopes[w.g * a.r + w.hb * a.H + h] * kLog2e;
+        if (bias) slope2 = a.mod.slopes[w.g * a.r + w.hb * a.H + h] * kLog2e;
       }
     }
     const long long orow = ((long long)w.b * a.h_q + w.g * a.r + w.hb * a.H + h) * a.S_q + qi;
@@ -431,8 +437,8 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
                        (kWin && (long long)key0 <= pos_max - win);
       if constexpr (kMod) {
         need_mask = __any_sync(0xffffffffu, store_row && (key0 <= win_last || key0 + kBN - 1 > key_last));
-        if (cap) tanh_scores<kBN>(sr, a.mod.k1);
-        if (bias) {
+        if constexpr (cap) tanh_scores<kBN>(sr, a.mod.k1);
+        if constexpr (bias) {
           // distances key - pos from the block's first key on (exact below 2^24); under the causal mask, and where
           // the block lies on one side of every row, the bias is linear along the block
           const float away = (float)(key0 - pos);
@@ -680,7 +686,7 @@ using tc::elect_one;
 // are built once: the start address sits in the low 14 bits (address >> 4, below 2^14 for any
 // shared-memory address), so the descriptor of base + offset is the base's descriptor plus
 // offset >> 4.
-template <int D, bool kSplit, bool kMod>
+template <int D, bool kSplit, int kMod>
 __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, uint32_t sQ,
                                          uint32_t sK, uint32_t sV, uint64_t* bars,
                                          volatile int* abort) {
@@ -788,7 +794,7 @@ __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, u
   wait_bar(bar(kBarDone + t), 0, &no_abort, a.err);
 }
 
-template <int D, bool kWin, bool kSplit, bool kMod>
+template <int D, bool kWin, bool kSplit, int kMod>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_bf16_kernel(const __grid_constant__ CUtensorMap tmq,
                         const __grid_constant__ CUtensorMap tmk,
@@ -950,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kWin, bool kSplit, bool kMod = false>
+template <int D, bool kWin, bool kSplit, int kMod = 0>
 cudaError_t launch_typed(const PArgs& p, const CUtensorMap* tmaps, long long ctas, cudaStream_t s) {
   auto kern = prefill_bf16_kernel<D, kWin, kSplit, kMod>;
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
@@ -1016,11 +1022,22 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
       if (e != cudaSuccess) return e;
       p.mod.hull = hull;
     }
-    if (a.d_h == 128) return p.split ? pf::launch_typed<128, false, true, true>(p, tmaps, ctas, s)
-                                     : pf::launch_typed<128, false, false, true>(p, tmaps, ctas, s);
-    if (a.d_h == 64) return p.split ? pf::launch_typed<64, false, true, true>(p, tmaps, ctas, s)
-                                    : pf::launch_typed<64, false, false, true>(p, tmaps, ctas, s);
-    return cudaErrorInvalidValue;
+    const bool cap = a.mod.softcap > 0.f, bias = a.mod.slopes != nullptr;
+    auto launch = [&](auto kind) {
+      constexpr int K = decltype(kind)::value;
+      if (a.d_h == 128) return p.split ? pf::launch_typed<128, false, true, K>(p, tmaps, ctas, s)
+                                       : pf::launch_typed<128, false, false, K>(p, tmaps, ctas, s);
+      if (a.d_h == 64) return p.split ? pf::launch_typed<64, false, true, K>(p, tmaps, ctas, s)
+                                      : pf::launch_typed<64, false, false, K>(p, tmaps, ctas, s);
+      return cudaErrorInvalidValue;
+    };
+    using pf::kModBias;
+    using pf::kModCap;
+    using pf::kModOn;
+    if (cap && bias) return launch(std::integral_constant<int, kModOn + kModCap + kModBias>());
+    if (cap) return launch(std::integral_constant<int, kModOn + kModCap>());
+    if (bias) return launch(std::integral_constant<int, kModOn + kModBias>());
+    return launch(std::integral_constant<int, kModOn>());
   }
   if (a.d_h == 128) {
     if (p.split) return win ? pf::launch_typed<128, true, true>(p, tmaps, ctas, s)
