@@ -494,7 +494,7 @@ gqa_status gqa_prefill_mod(const void* q, const void* k_cache, const void* v_cac
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == GQA_FP32) return from_cuda(launch_prefill_fp32(a, s));
+  if (dtype == GQA_FP32) return from_cuda(a.mod.on() ? launch_prefill_fp32_mod(a, s) : launch_prefill_fp32(a, s));
   // TMA views: Q as (d_h, S_q, B*h_q) with box (64, P, H): one box holds the H heads x P
   // positions of a tile, head-major; K, V as rows (B*h_kv*T_max, d_h) with box (64, 128).
   const int H = prefill_heads_per_tile(h_q, h_kv);
@@ -588,7 +588,7 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == GQA_FP32) return from_cuda(launch_backward_fp32(a, s));
+  if (dtype == GQA_FP32) return from_cuda(a.mod.on() ? launch_backward_fp32_mod(a, sm_count(), s) : launch_backward_fp32(a, s));
   // TMA views: Q and dO as (d_h, S_q, B*h_q) with box (64, 64, 1) for the key-stationary dK/dV
   // kernel and (64, P, H) for the query-stationary dQ kernel; K, V as rows with box (64, 128) for
   // dK/dV (its 128 stationary keys) and (64, 64) for dQ (its 64-key blocks).

@@ -6,7 +6,6 @@
 //   p_ij = exp(scale q_i.k_j - lse_i),  dp_ij = dO_i.v_j,  ds_ij = p_ij (dp_ij - D_i),
 //   dQ_i = scale sum_j ds_ij k_j,  dK_j = scale sum_{a in group, i} ds_ij q_i,
 //   dV_j = sum_{a in group, i} p_ij dO_i
-// With a cap the score's own derivative 1 - tanh^2 multiplies ds; a distance bias is constant.
 // [序列计算与存储, the paragraph after the 两块算例 listing; 第三章, section 3.5].
 //   dq kernel    one warp per query row; lanes split d_h
 //   dkdv kernel  one warp per (sequence, KV head, key); it walks every row of every head of the
@@ -28,12 +27,8 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Does row i of sequence b (at position pos) see the key?
-__device__ __forceinline__ bool seen(const BackwardArgs& a, int b, int i, int key, long long pos, int kv) {
-  if (key >= kv || (a.causal && key > pos) || (a.window > 0 && key <= pos - a.window)) return false;
-  if (!a.mod.range) return true;
-  const int32_t* rg = a.mod.range + ((long long)b * a.S_q + i) * 2;
-  return key >= rg[0] && key < rg[1];
+__device__ __forceinline__ bool seen(long long key, long long pos, int kv, int causal, int window) {
+  return key < kv && (!causal || key <= pos) && (window == 0 || key > pos - window);
 }
 
 __global__ void __launch_bounds__(256) rowterm_fp32_kernel(BackwardArgs a) {
@@ -72,7 +67,6 @@ __global__ void __launch_bounds__(256) dq_fp32_kernel(BackwardArgs a) {
   const float* vp = reinterpret_cast<const float*>(a.v) + kvb;
   const float dr = a.drow[w];
   const long long pos = (long long)qs + i;
-  const float slope = a.mod.slopes ? a.mod.slopes[head] : 0.f;
   float qr[kMaxPerLane], dor[kMaxPerLane], acc[kMaxPerLane];
 #pragma unroll
   for (int e = 0; e < kMaxPerLane; ++e) {
@@ -82,7 +76,7 @@ __global__ void __launch_bounds__(256) dq_fp32_kernel(BackwardArgs a) {
     acc[e] = 0.f;
   }
   for (int j = 0; j < kv; ++j) {
-    if (!seen(a, b, i, j, pos, kv)) continue;
+    if (!seen(j, pos, kv, a.causal, a.window)) continue;
     const float* kj = kp + (long long)j * D;
     const float* vj = vp + (long long)j * D;
     float s = 0.f, dp = 0.f;
@@ -96,9 +90,8 @@ __global__ void __launch_bounds__(256) dq_fp32_kernel(BackwardArgs a) {
     }
     s = warp_sum(s);
     dp = warp_sum(dp);
-    float t;
-    const float p = expf(mod_score(s, a.scale, a.mod.softcap, slope, pos - j, &t) - lse);
-    const float ds = p * (dp - dr) * (1.f - t * t);
+    const float p = expf(s * a.scale - lse);
+    const float ds = p * (dp - dr);
 #pragma unroll
     for (int e = 0; e < kMaxPerLane; ++e) {
       const int c = lane + 32 * e;
@@ -141,9 +134,8 @@ __global__ void __launch_bounds__(256) dkdv_fp32_kernel(BackwardArgs a) {
     for (int hl = 0; hl < r; ++hl) {
       const int head = g * r + hl;
       const long long base = ((long long)b * a.h_q + head) * a.S_q;
-      const float slope = a.mod.slopes ? a.mod.slopes[head] : 0.f;
       for (int i = 0; i < a.S_q; ++i) {
-        if (!seen(a, b, i, j, (long long)qs + i, kv)) continue;
+        if (!seen(j, (long long)qs + i, kv, a.causal, a.window)) continue;
         const float lse = a.lse[base + i];
         if (!(lse > -INFINITY)) continue;
         const float* q = reinterpret_cast<const float*>(a.q) + (base + i) * D;
@@ -159,9 +151,8 @@ __global__ void __launch_bounds__(256) dkdv_fp32_kernel(BackwardArgs a) {
         }
         s = warp_sum(s);
         dp = warp_sum(dp);
-        float t;
-        const float p = expf(mod_score(s, a.scale, a.mod.softcap, slope, (long long)qs + i - j, &t) - lse);
-        const float ds = p * (dp - a.drow[base + i]) * (1.f - t * t);
+        const float p = expf(s * a.scale - lse);
+        const float ds = p * (dp - a.drow[base + i]);
 #pragma unroll
         for (int e = 0; e < kMaxPerLane; ++e) {
           const int c = lane + 32 * e;

@@ -135,6 +135,7 @@ struct PrefillArgs {
 };
 // fp32 check mode (scalar FFMA)
 cudaError_t launch_prefill_fp32(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, cudaStream_t s);  // modified scores
 // bf16 tcgen05 path (sm_100a). tmaps: [0] = Q as a 3-D view (d_h, S_q, B*h_q) with box
 // (64, 128 / H, H); [1] = K, [2] = V as 2-D views (d_h, B*h_kv*T_max) with box (64, 128).
 cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, int num_sms,
@@ -170,6 +171,7 @@ struct BackwardArgs {
 cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps, int num_sms,
                                  cudaStream_t s);
 cudaError_t launch_backward_fp32(const BackwardArgs& a, cudaStream_t s);
+cudaError_t launch_backward_fp32_mod(const BackwardArgs& a, int num_sms, cudaStream_t s);  // modified scores
 size_t backward_hull_bytes(int B, int h_q, int h_kv, int S_q);  // BackwardArgs::hull
 size_t prefill_hull_bytes(int B, int h_q, int h_kv, int S_q);   // PrefillArgs::workspace
 

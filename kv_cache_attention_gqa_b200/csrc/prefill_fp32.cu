@@ -10,7 +10,6 @@
 // the online-softmax update with a block of one key:
 //   m' = max(m, s_j),  l' = e^{m - m'} l + e^{s_j - m'},  u' = e^{m - m'} u + e^{s_j - m'} v_j
 // [序列计算与存储, section 在线 softmax], starting from m = -inf, l = 0, u = 0; o = u / l.
-// With modified scores s_j is capped and biased first, and a row's key range narrows the keys.
 
 #include "common.cuh"
 #include "internal.h"
@@ -42,7 +41,6 @@ __global__ void __launch_bounds__(256) prefill_fp32_kernel(PrefillArgs a) {
   const int kv_len = a.kv_len ? a.kv_len[b] : a.T_max;
   const int q0 = a.q_start ? a.q_start[b] : 0;
   int n_vis = -1, j_lo = 0;
-  const bool ranged = a.mod.range != nullptr;
   if (kv_len < 1 || kv_len > a.T_max) {
     if (lane == 0) set_device_error(a.err, GQA_DEVERR_KV_LEN);
   } else if (q0 < 0) {
@@ -55,15 +53,9 @@ __global__ void __launch_bounds__(256) prefill_fp32_kernel(PrefillArgs a) {
       if (lo > 0) j_lo = lo < n_vis ? (int)lo : n_vis;
       n_vis -= j_lo;
     }
-    if (ranged) {  // the row's own keys, within those
-      const int32_t* rg = a.mod.range + ((long long)b * a.S_q + i) * 2;
-      const int end = min(j_lo + n_vis, max(rg[1], 0));
-      j_lo = max(j_lo, rg[0]);
-      n_vis = max(0, end - j_lo);
-    }
   }
   if (n_vis <= 0) {  // invalid request or no visible key: zero row, flagged
-    if (n_vis == 0 && lane == 0 && !ranged) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+    if (n_vis == 0 && lane == 0) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
     for (int c = lane; c < D; c += 32) o[c] = 0.f;
     if (a.lse && lane == 0) a.lse[warp] = -INFINITY;
     return;
@@ -77,7 +69,6 @@ __global__ void __launch_bounds__(256) prefill_fp32_kernel(PrefillArgs a) {
     acc[e] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
-  const float slope = a.mod.slopes ? a.mod.slopes[head] : 0.f;
   for (int j = j_lo; j < j_lo + n_vis; ++j) {
     const float* kj = kp + (long long)j * D;
     const float* vj = vp + (long long)j * D;
@@ -89,8 +80,7 @@ __global__ void __launch_bounds__(256) prefill_fp32_kernel(PrefillArgs a) {
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-    float t;
-    const float s = mod_score(part, a.scale, a.mod.softcap, slope, (long long)q0 + i - j, &t);
+    const float s = part * a.scale;
     const float m_new = fmaxf(m, s);
     const float alpha = expf(m - m_new);  // 0 on the first key (m = -inf)
     const float p = expf(s - m_new);
