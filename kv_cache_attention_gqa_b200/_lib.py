@@ -9,6 +9,7 @@ fallback: if the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -542,25 +543,30 @@ def _on_device(*ts):
     """Every tensor given is a CUDA tensor on the current device (as _need_cuda, for strided inputs)."""
     dev = torch.cuda.current_device()
     for t in ts:
-        if t is None:
+        if t is None or t.get_device() == dev:
             continue
         if not t.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
-        if t.get_device() != dev:
-            raise ValueError(f"tensors must live on the current CUDA device (cuda:{dev}), not {t.device}")
+        raise ValueError(f"tensors must live on the current CUDA device (cuda:{dev}), not {t.device}")
 
 
 def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
     """A (B, heads, S, d) tensor whose rows have adjacent elements; the other strides are free."""
     if t.dim() != 4:
         raise ValueError(f"{name} must have the dimensions (B, heads, S, d)")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if t.stride(3) != 1 and t.shape[3] > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent (last stride 1)")
     return t
 
 
+@functools.lru_cache(maxsize=1024)
+def _stride_array(strides):
+    return (ctypes.c_int64 * 3)(*strides[:3])
+
+
 def _strides(t: torch.Tensor):
-    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+    """Host int64[3] of t's strides (read-only; one array per distinct strides)."""
+    return _stride_array(t.stride())
 
 
 def _positions(positions, B: int, S: int, device, name: str):
@@ -629,7 +635,7 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions, *, offset: int = 0,
     dt = _dtype_code(x)
     inv_freq = _inv_freq(inv_freq, d, offset)
     if out is None:
-        out = torch.empty((B, h, S, d), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _rows(_out(out, x.shape, x.dtype, x.device), "out")
         if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())):
@@ -646,26 +652,32 @@ def rope(x: torch.Tensor, inv_freq: torch.Tensor, positions, *, offset: int = 0,
 def _rope_append(q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, positions, offset, q_out):
     """Checks and arguments shared by kv_rope_append and kv_rope_append_paged."""
     _on_device(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out)
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and (q_out is None or q_out.is_contiguous())):
-        raise ValueError("the caches and q_out must be contiguous (row-major)")
-    for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
-        _rows(t, name)
+    _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new")
     B, h_q, S, dq = q.shape
     if v_cache.shape != k_cache.shape:
         raise ValueError("the K and V caches must have one shape")
-    if dq != d or tuple(k_new.shape) != (B, h_kv, S, d) or v_new.shape != k_new.shape:
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous (row-major)")
+    new = (B, h_kv, S, d)
+    if dq != d or k_new.shape != new or v_new.shape != new:
         raise ValueError("q must be (B, h_q, S, d) and k_new, v_new (B, h_kv, S, d)")
-    dt = _dtype_code(q)
-    if any(t.dtype != q.dtype for t in (k_new, v_new, k_cache, v_cache)):
+    dtype = q.dtype
+    if k_new.dtype != dtype or v_new.dtype != dtype or k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError("q, k_new, v_new and the caches must share one dtype")
+    dt = _dtype_code(q)
     inv_freq = _inv_freq(inv_freq, d, offset)
     pos_t = _int_vec(pos, B, q.device, "pos")
     if pos_t is None:
         raise ValueError("pos must be given")
     at, per_token = (None, 0) if positions is None else _positions(positions, B, S, q.device, "positions")
-    q_out = _out(q_out, (B, h_q, S, d), q.dtype, q.device)
-    if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
-        raise ValueError("in place, q must be contiguous")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _out(q_out, (B, h_q, S, d), dtype, q.device)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous (row-major)")
+        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("in place, q must be contiguous")
     return B, h_q, S, dt, inv_freq, pos_t, at, per_token, q_out
 
 
@@ -780,8 +792,12 @@ def _evict_args(k, v, weights, B, h_kv, T_max, T_out, budget, kv_len, weights_ou
             raise ValueError("weights_out must be given when the caches are not shortened in place")
         weights_out = weights
     _out(weights_out, (B, h_kv, T_out), torch.float32, weights.device)
-    kept = _out(kept, (B, h_kv, budget), torch.int32, weights.device)
-    new_len = torch.empty(B, dtype=torch.int32, device=weights.device)
+    if kept is None:  # one allocation for both
+        small = torch.empty(B * (h_kv * budget + 1), dtype=torch.int32, device=weights.device)
+        kept, new_len = small[B:].view(B, h_kv, budget), small[:B]
+    else:
+        kept = _out(kept, (B, h_kv, budget), torch.int32, weights.device)
+        new_len = torch.empty(B, dtype=torch.int32, device=weights.device)
     return dt, budget, weights_out, kept, new_len, _int_vec(kv_len, B, weights.device, "kv_len")
 
 
