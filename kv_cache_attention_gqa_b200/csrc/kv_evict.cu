@@ -3,21 +3,27 @@
 // moved to the front, in their order, in the caller's cache (in place) or into another.
 //
 // Two launches.
-//   select  one CTA per (sequence, KV head). The threshold weight is found by a radix selection over the
+//   select  one CTA, or for long rows a cluster of them, per (sequence, KV head); each keeps its share of the keys. The threshold weight is found by a radix selection over the
 //           weights' bits mapped to unsigned integers of the same order: passes of 11, 11 and 10 bits, each a
 //           histogram in shared memory and a scan of its counts (with 8 bits the first pass would be the
 //           exponent alone, a handful of bins that every thread of a warp adds to in turn); the weights are
-//           read from DRAM once and kept in shared memory while they fit. Then one pass over the keys in
+//           read from DRAM once and kept in shared memory while they fit. The blocks of a cluster read each
+//           other's counts (distributed shared memory) and find the same threshold. Then one pass over the keys in
 //           order writes the kept indices: everything above the threshold, and of the keys equal to it the
 //           first ones. Bound by latency: a few thousand keys per block, a dozen dependent phases.
 //   move    rows of K, V and the weights, bound by DRAM (kept rows once in, once out). Kept indices ascend, so
 //           a row's source is at or behind its destination (kept[i] >= i): moving in order, batch by batch,
 //           with every load of a batch before its first store, never overwrites a row still to be read, also
 //           in place. Columns are independent, so a (sequence, head, tensor) is cut into column slices,
-//           one CTA each, which need no order among them; a copy into another contiguous cache is cut along
+//           one CTA each, which need no order among them; a copy into another cache or other pages is cut along
 //           the rows too. The next batch's loads are issued before the current batch's stores (its sources lie
 //           behind the current destinations).
+//
+// Measured (B200, d = 128 bf16): 64 rows of 8192 keys to 2048: 39 us (select 13, move 26 for 134 MB); 32 rows of 3001 to
+// 32768 keys to 4096, 16-key pages: 44 us (select 18, move 26); the moves cut along the rows into 4 blocks an SM (8:
+// 39.5 / 46.7 us, 16: 40.1 / 49.1 us).
 
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -26,9 +32,12 @@
 namespace gqa {
 namespace ev {
 
+namespace cg = cooperative_groups;
+
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeep = 48 * 1024;  // weights kept in shared memory (192 KiB)
+constexpr int kMinShare = 4096;  // keys of a block of a cluster, at least
 constexpr int kBins = 2048;  // 11 bits a pass: two bins a thread
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // vectors in flight per thread and batch
@@ -44,28 +53,33 @@ __device__ __forceinline__ uint32_t rank_bits(float w) {
 __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint4 keep4[];  // ranks of the competing keys, when they fit (a whole number of fours)
   uint32_t* const keep = reinterpret_cast<uint32_t*>(keep4);
-  __shared__ int hist[kBins];
+  __shared__ int hists[3][kBins];  // one per pass: the cluster reads a pass's counts while the next pass counts
+  __shared__ int totals[2];        // this block's keys above the threshold, and equal to it
   __shared__ int warp_sum[kSelWarps], warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int g = blockIdx.x % a.h_kv, b = blockIdx.x / a.h_kv;
-  const long long bg = blockIdx.x;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank_ = (int)cluster.block_rank();
+  const int g = blockIdx.x / ranks % a.h_kv, b = blockIdx.x / ranks / a.h_kv;
+  const long long bg = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = a.kv_len ? a.kv_len[b] : a.T_max;
   const bool valid = n >= 0 && n <= a.T_max;
   int32_t* kept = a.kept + bg * a.budget;
   const int len = !valid ? 0 : n < a.budget ? n : a.budget;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && rank_ == 0) {
     if (!valid && g == 0) set_device_error(a.err, GQA_DEVERR_KV_LEN);
     if (g == 0) a.new_len[b] = valid ? len : n;
   }
-  if (!valid || n <= a.budget) {  // everything stays
-    for (int i = threadIdx.x; i < a.budget; i += kSelThreads) kept[i] = i < len ? i : -1;
+  if (!valid || n <= a.budget) {  // everything stays (the whole cluster takes this way)
+    for (int i = rank_ * kSelThreads + threadIdx.x; i < a.budget; i += ranks * kSelThreads) kept[i] = i < len ? i : -1;
     return;
   }
   const float* w = a.w + bg * a.T_max;
-  const int lo = a.sink, hi = n - a.recent, m = hi - lo;  // the keys that compete: [lo, hi)
-  const int need = a.budget - a.sink - a.recent;          // of which so many stay (need < m)
+  // the keys that compete, [lo0, hi0), and this block's share of them, [lo, lo + m)
+  const int lo0 = a.sink, hi0 = n - a.recent, share = ((hi0 - lo0 + ranks - 1) / ranks + 3) / 4 * 4;
+  const int lo = min(hi0, lo0 + rank_ * share), m = min(hi0 - lo, share);
+  const int need = a.budget - a.sink - a.recent;          // of which so many stay (fewer than compete)
   const bool fits = m <= kSelKeep;
   auto rank = [&](int i) { return fits ? keep[i] : rank_bits(__ldg(w + lo + i)); };
   if (fits) {
@@ -79,8 +93,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
         if (i0 + u * kSelThreads < m) keep[i0 + u * kSelThreads] = rank_bits(x[u]);
     }
   }
-  for (int i = threadIdx.x; i < a.sink; i += kSelThreads) kept[i] = i;
-  for (int i = threadIdx.x; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = hi + i;
+  if (rank_ == 0) {
+    for (int i = threadIdx.x; i < a.sink; i += kSelThreads) kept[i] = i;
+    for (int i = threadIdx.x; i < a.recent; i += kSelThreads) kept[a.budget - a.recent + i] = hi0 + i;
+  }
   if (need == 0) return;
 
   // threshold: the need-th largest rank, 11, 11 and 10 bits at a time
@@ -89,6 +105,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+    int* const hist = hists[pass];
     for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     const uint32_t mask = (1u << (top - shift)) - 1u;
@@ -116,9 +133,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
           if (bin[e] >= 0) atomicAdd(&hist[bin[e]], 1);
       }
     }
-    __syncthreads();
-    // thread t holds bins 2047 - 2t and 2046 - 2t; counts of the bins above them by a scan over the block
-    const int c0 = hist[kBins - 1 - 2 * threadIdx.x], c1 = hist[kBins - 2 - 2 * threadIdx.x];
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
+    // thread t holds bins 2047 - 2t and 2046 - 2t of all blocks; counts of the bins above them by a scan
+    int c0 = 0, c1 = 0;
+    for (int k = 0; k < ranks; ++k) {
+      const int2 c = *reinterpret_cast<const int2*>((ranks > 1 ? cluster.map_shared_rank(hist, k) : hist) + kBins - 2 -
+                                                    2 * threadIdx.x);
+      c0 += c.y;
+      c1 += c.x;
+    }
     int above = c0 + c1;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -155,6 +179,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) kv_evict_select_kernel(const _
   }
   __syncthreads();
   int gt0 = 0, eq0 = 0;  // before this warp's range
+  if (ranks > 1) {
+    if (threadIdx.x == 0) {
+      totals[0] = totals[1] = 0;
+      for (int k = 0; k < kSelWarps; ++k) {
+        totals[0] += warp_gt[k];
+        totals[1] += warp_eq[k];
+      }
+    }
+    cluster.sync();
+    for (int k = 0; k < rank_; ++k) {
+      const int* other = cluster.map_shared_rank(totals, k);
+      gt0 += other[0];
+      eq0 += other[1];
+    }
+    cluster.sync();  // no block leaves while its counts may be read
+  }
   for (int k = 0; k < warp; ++k) {
     gt0 += warp_gt[k];
     eq0 += warp_eq[k];
@@ -208,9 +248,12 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const __gri
   const int rows = kMoveThreads / slice;                  // rows a block moves at once
   const int rl = threadIdx.x / slice, c = threadIdx.x - rl * slice;
   const bool lane_ok = rl < rows && c < nc;
-  // rows [r0, r1) of this block (a move that may be in place is never cut along the rows)
-  const int per = (len + row_split - 1) / row_split;
-  const int r0 = min(len, part * per), r1 = min(len, r0 + per);
+  // rows [r0, r1) of this block. A move in place (onto the same rows, or by a table that begins with the sequence's
+  // own pages) has an order: its first block takes all rows.
+  const bool ordered =
+      a.in_place || (a.block_table && a.block_table_out[(long long)b * a.max_pages_out] == a.block_table[(long long)b * a.max_pages]);
+  const int per = ordered ? (part == 0 ? len : 0) : (len + row_split - 1) / row_split;
+  const int r0 = ordered ? 0 : min(len, part * per), r1 = min(len, r0 + per);
   // Source and destination rows, a table of kTable at a time (dst < 0: not moved). Every thread of a row
   // working them out for itself, kept index, table entry and divisions, was the longer part of the kernel.
   __shared__ int s_src[2][kTable], s_dst[2][kTable];
@@ -279,10 +322,10 @@ template <typename Vec>
 cudaError_t launch_move(const EvictArgs& a, long long row_bytes, int num_sms, cudaStream_t s) {
   const int vecs = (int)(row_bytes / sizeof(Vec));
   const long long bg = (long long)a.B * a.h_kv;
-  // Column slices (a power of two of vectors). An in-place or paged move has only these to share: 128 bytes where
-  // that gives every SM two blocks, down to 32 (a DRAM sector) where not. A copy into another contiguous
-  // cache has no order and is cut along the rows instead: whole rows up to 256 bytes.
-  const bool ordered = a.in_place || a.block_table;
+  // Column slices (a power of two of vectors). A move in place has only these to share: 128 bytes where that gives
+  // every SM two blocks, down to 32 (a DRAM sector) where not. A copy into another cache or other pages has no
+  // order and is cut along the rows instead: whole rows up to 256 bytes.
+  const bool ordered = a.in_place;
   int slice = (ordered ? 128 : 256) / (int)sizeof(Vec);
   const int least = 32 / (int)sizeof(Vec);
   auto slices = [&](int w) { return (vecs + w - 1) / w; };
@@ -293,7 +336,7 @@ cudaError_t launch_move(const EvictArgs& a, long long row_bytes, int num_sms, cu
   if (!ordered) {
     const int rows = kMoveThreads / slice * kMoveUnroll;
     const int most = (a.budget + rows - 1) / rows;
-    const long long want = (16ll * num_sms + bg * 2 * n_slices - 1) / (bg * 2 * n_slices);
+    const long long want = (4ll * num_sms + bg * 2 * n_slices - 1) / (bg * 2 * n_slices);
     split = (int)(want < most ? want : most);
     if (split < 1) split = 1;
   }
@@ -328,9 +371,25 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int d_h, int elem_bytes, int num
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int keep = a.T_max < ev::kSelKeep ? a.T_max : ev::kSelKeep;
-  ev::kv_evict_select_kernel<<<(unsigned)(a.B * a.h_kv), ev::kSelThreads, (size_t)(keep + 3) / 4 * 16, s>>>(a);
-  e = cudaGetLastError();
+  // Blocks per row: up to 8, each with kMinShare keys at least, while every block has an SM (one fills it; a
+  // second wave costs more than the split gains). 32 rows of 3001 to 32768 keys: 1, 4, 8 blocks 30.7, 17.7, 35 us; 64
+  // rows of 8192: 1, 2, 4 blocks 13.2, 13.2, 26 us.
+  const long long bg = (long long)a.B * a.h_kv;
+  int ranks = 1;
+  while (ranks < 8 && a.T_max / (2 * ranks) >= ev::kMinShare && 2 * ranks * bg <= num_sms) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(bg * ranks));
+  cfg.blockDim = dim3(ev::kSelThreads);
+  const int share = (a.T_max + ranks - 1) / ranks;  // a block's ranks, a whole number of fours
+  cfg.dynamicSmemBytes = (size_t)((share < ev::kSelKeep ? share : ev::kSelKeep) + 3) / 4 * 16;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, ev::kv_evict_select_kernel, a);
   if (e != cudaSuccess) return e;
   const long long row_bytes = (long long)d_h * elem_bytes;
   const uintptr_t all = (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.k_out | (uintptr_t)a.v_out;
