@@ -319,19 +319,30 @@ gqa_status kv_weights_impl(KvWeightsArgs a, gqa_dtype dtype, size_t workspace_by
   if (dtype == GQA_FP32) return from_cuda(launch_kv_weights_fp32(a, s));
   const KvWeightsTile t = kv_weights_tile(a.h_q, a.h_kv, a.S_q);
   CUtensorMap maps[2];
-  const uint64_t kdims[2] = {(uint64_t)a.d_h, (uint64_t)k_rows};
   const uint64_t strides[1] = {(uint64_t)a.d_h * 2};
-  const uint32_t kbox[2] = {64, (uint32_t)kv_weights_sub(a.block_table != nullptr, a.page_size)};
-  if (!encode_bf16(&maps[0], a.k, 2, kdims, strides, kbox)) return GQA_ERR_CUDA;
+  const uint32_t sub = (uint32_t)kv_weights_sub(a.block_table != nullptr, a.page_size);
   bool ok;
+  if (kv_weights_4d(a.block_table != nullptr, a.d_h)) {
+    // groups of 8 rows (pages hold whole ones) with their two 64-column chunks side by side
+    const uint64_t dims[4] = {64, 8, 2, (uint64_t)k_rows / 8};
+    const uint64_t strides4[3] = {256, 128, 2048};
+    const uint32_t box[4] = {64, 8, 2, sub / 8};
+    ok = encode_bf16(&maps[0], a.k, 4, dims, strides4, box);
+  } else {
+    const uint64_t kdims[2] = {(uint64_t)a.d_h, (uint64_t)k_rows};
+    const uint32_t kbox[2] = {64, sub};
+    ok = encode_bf16(&maps[0], a.k, 2, kdims, strides, kbox);
+  }
+  if (!ok) return GQA_ERR_CUDA;
   if (t.small) {
     const uint64_t qdims[2] = {(uint64_t)a.d_h, (uint64_t)a.B * a.h_q * a.S_q};
     const uint32_t qbox[2] = {64, (uint32_t)t.rows};
     ok = encode_bf16(&maps[1], a.q, 2, qdims, strides, qbox);
   } else {
-    const uint64_t qdims[3] = {(uint64_t)a.d_h, (uint64_t)a.S_q, (uint64_t)a.B * a.h_q};
-    const uint64_t qstrides[2] = {(uint64_t)a.d_h * 2, (uint64_t)a.S_q * a.d_h * 2};
-    const uint32_t qbox[3] = {64, (uint32_t)t.P, (uint32_t)t.H};
+    const uint64_t rows = (uint64_t)a.B * a.h_q;
+    const uint64_t qdims[3] = {(uint64_t)a.d_h, t.flat ? rows * a.S_q : (uint64_t)a.S_q, t.flat ? 1 : rows};
+    const uint64_t qstrides[2] = {(uint64_t)a.d_h * 2, qdims[1] * a.d_h * 2};
+    const uint32_t qbox[3] = {64, t.flat ? 128u : (uint32_t)t.P, t.flat ? 1u : (uint32_t)t.H};
     ok = encode_bf16(&maps[1], a.q, 3, qdims, qstrides, qbox);
   }
   if (!ok) return GQA_ERR_CUDA;

@@ -80,17 +80,19 @@ struct KvWeightsArgs {
   int max_pages = 0, page_size = 0, num_pages = 0;
   unsigned* err;
 };
-// Q tile of the bf16 kernels: P positions x H heads, or with up to 32 rows a group (small) `rows` adjacent
-// rows; keys per K copy
+// Q tile of the bf16 kernels: P positions x H heads; flat: 128 adjacent rows; small (up to 32 rows a group): `rows`
+// adjacent rows. And the keys per K copy.
 struct KvWeightsTile {
-  bool small;
+  bool small, flat;
   int P, H, rows;
 };
 KvWeightsTile kv_weights_tile(int h_q, int h_kv, int S_q);
 int kv_weights_sub(bool paged, int page_size);
+bool kv_weights_4d(bool paged, int d_h);  // K map as (64, 8 rows, 2 chunks, rows / 8), box (64, 8, 2, sub / 8)
 size_t kv_weights_workspace_bytes(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype, int num_sms);
 // tmaps: [0] K rows as a 2-D view (d_h, rows) with box (64, kv_weights_sub); [1] queries: small, as a 2-D
-// view (d_h, B*h_q*S_q) with box (64, rows), else as a 3-D view (d_h, S_q, B*h_q) with box (64, P, H);
+// view (d_h, B*h_q*S_q) with box (64, rows), flat, as (d_h, B*h_q*S_q, 1) with box (64, 128, 1), else as
+// (d_h, S_q, B*h_q) with box (64, P, H);
 // SWIZZLE_128B.
 cudaError_t launch_kv_weights_bf16(const KvWeightsArgs& a, const CUtensorMap* tmaps, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_weights_fp32(const KvWeightsArgs& a, cudaStream_t s);

@@ -8,7 +8,8 @@
 // A unit of work is 256 keys of one (sequence, KV head) against the query rows that see them (all of them,
 // or one of `parts` shares of them). The keys of a K tile sit on the 128 TMEM lanes, S^T = K Q^T (tcgen05.mma, A = K tile, B = Q tile, both K-major in shared memory), so
 // the sum over rows runs along the columns a thread reads of its own lane: no exchange between threads, no
-// atomics, the same result every time. A Q tile is up to 128 columns: P positions of H heads.
+// atomics, the same result every time. A Q tile is 128 columns: positions of one head, or with
+// fewer than 128 positions the rows of the group's heads end to end.
 // Bound by the exponentials (one per visible pair, 16 a clock and SM: 2048 clocks per 256 x 128 tile) and
 // the MMAs, which run at 1650 clocks per tile instead of 1024 because both operands come from shared memory
 // and fill its 128 bytes a clock by themselves. Four warpgroups: one per 128 keys and half of the columns;
@@ -47,7 +48,7 @@ constexpr int kBK = 128;  // keys of a K tile (= TMEM lanes)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSeqTable = 1024;  // sequences whose length and first position are kept in shared memory
 constexpr int kFar = 0x7ffffffe;  // the position of a row that sees every key (no causal mask)
-constexpr int kUnitsPerSm = 12;   // units wanted per SM before query rows are cut into parts
+constexpr int kUnitsPerSm = 6;    // units wanted per SM before query rows are cut into parts
 constexpr int kTilesPerPart = 4;  // a part holds at least this many Q tiles (of the fullest unit)
 
 struct WArgs {
@@ -58,6 +59,7 @@ struct WArgs {
   int B, h_q, h_kv, r, S_q, T_max;
   int P, H, hblocks, npb;  // Q tile: P positions x H heads; blocks of heads, of positions
   int N;                   // MMA columns of a Q tile: P H rounded up to 16 (the rest is masked)
+  int flat;                // 1 (S_q < 128): a Q tile is 128 of the group's r S_q rows, which lie end to end
   int nkt;                 // units along the keys of a sequence
   int parts;
   int n_units;
@@ -68,6 +70,11 @@ struct WArgs {
   int part_keys;
   const int32_t* block_table;
   int max_pages, page_size, num_pages, sub;  // sub: keys per K copy (128, or 64 / 16 on a paged cache)
+  // Where a K tile's rows lie in shared memory: `k_chunk` bytes between its 64-column chunks, `k_group` between
+  // groups of 8 rows. Plane by plane (16384, 1024), or on a paged cache with d = 128 both chunks of a group side by
+  // side (1024, 2048): the copy of a sub-tile is then one box of four dimensions instead of one per chunk
+  // (16 copies of 2 KB a tile were the bound of paged calls: 54 us for the case below).
+  int k_chunk, k_group, k_4d;
   unsigned* err;
 };
 
@@ -147,6 +154,18 @@ __device__ __forceinline__ Unit make_unit(const WArgs& a, const int2* seq, int i
   u.t0 = a.div_parts.div(n * u.part);
   u.t1 = a.div_parts.div(n * (u.part + 1));
   return u;
+}
+
+// Sub-tile `sub` (a.sub rows from `row` of the cache on) of a K tile.
+template <int kNch>
+__device__ __forceinline__ void load_keys(const WArgs& a, uint32_t tile, const CUtensorMap* map, uint32_t bar, int sub,
+                                          int row) {
+  if (a.k_4d) {
+    tma_load_4d(tile + sub * (a.sub / 8) * a.k_group, map, bar, 0, 0, 0, row / 8);
+  } else {
+#pragma unroll
+    for (int ch = 0; ch < kNch; ++ch) tma_load_2d(tile + ch * a.k_chunk + sub * a.sub * 128, map, bar, ch * 64, row);
+  }
 }
 
 // CTA c of G takes units c, 2G - 1 - c, 2G + c, ...: a snake over the heaviest-first order.
@@ -283,12 +302,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (lane < n_sub) {
-#pragma unroll
-          for (int ch = 0; ch < C::kNch; ++ch)
-            tma_load_2d(sK + st * C::kKBytes + ch * C::kKChunk + lane * a.sub * 128, &tmk,
-                        bar(C::bKFull + st), ch * 64, row);
-        }
+        if (lane < n_sub) load_keys<C::kNch>(a, sK + st * C::kKBytes, &tmk, bar(C::bKFull + st), lane, row);
       }
       if (!ok) break;
       if (lane == 0) {
@@ -297,10 +311,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           const int st = nt % C::kQStages, f = nt / C::kQStages;
           if (f > 0) ok = wait_bar(bar(C::bQEmpty + st), (uint32_t)((f - 1) & 1), abort, a.err);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar(C::bQFull + st), (uint32_t)(C::kNch * a.P * a.H * 128));
+          const int head = u.b * a.h_q + u.g * a.r;
+          mbar_arrive_expect_tx(bar(C::bQFull + st), (uint32_t)(C::kNch * (a.flat ? kNQ : a.P * a.H) * 128));
           for (int ch = 0; ch < C::kNch; ++ch)
             tma_load_3d(sQ + st * C::kQBytes + ch * C::kQChunk, &tmq, bar(C::bQFull + st), ch * 64,
-                        (u.pb_lo + pb) * a.P, u.b * a.h_q + u.g * a.r + hb * a.H);
+                        a.flat ? head * a.S_q + t * kNQ : (u.pb_lo + pb) * a.P, a.flat ? 0 : head + hb * a.H);
           if (++pb == u.npb) {
             pb = 0;
             ++hb;
@@ -321,8 +336,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer ----------------------------------------------
-    const uint32_t idesc = tc::idesc_bf16(kBK, a.N, false);
-    const uint64_t dK = tc::smem_desc(sK, 16, 1024), dQ = tc::smem_desc(sQ, 16, 1024);
+    const int rows = a.r * a.S_q;
+    const uint64_t dK = tc::smem_desc(sK, 16, (uint32_t)a.k_group), dQ = tc::smem_desc(sQ, 16, 1024);
+    const uint64_t khi = dK & 0xffffffff00000000ull, khi_q = dQ & 0xffffffff00000000ull;
+    auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     auto wait = [&](int b_, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_bar(bar(b_), parity, abort, a.err)) != 0;
     };
@@ -343,14 +360,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
              (fb == 0 || wait(C::bFree + bf, (uint32_t)((fb - 1) & 1)));
         if (!ok) break;
         tc::fence_after_sync();
-        const uint64_t qd = dQ + (uint64_t)((st * C::kQBytes) >> 4);
+        // Everything an MMA takes is made warp-uniform first (the unit comes from shared memory, so the compiler
+        // cannot know it): the low words of the descriptors, which hold the address, the TMEM column and the shape.
+        const uint32_t ql = uniform((uint32_t)dQ + ((st * C::kQBytes) >> 4));
+        const uint32_t kl0 = uniform((uint32_t)dK + (((nk % C::kKStages) * C::kKBytes) >> 4));
+        const uint32_t kl1 = uniform((uint32_t)dK + ((((nk + 1) % C::kKStages) * C::kKBytes) >> 4));
+        const uint32_t col = uniform(tmem + bf * C::kBufCols), two = uniform(n_kt > 1 ? 1u : 0u);
+        const uint32_t idesc =
+            uniform(tc::idesc_bf16(kBK, a.flat ? min(kNQ, (rows - t * kNQ + 15) / 16 * 16) : a.N, false));
         if (tc::elect_one()) {
-          for (int kt = 0; kt < n_kt; ++kt) {
-            const uint64_t kd = dK + (uint64_t)((((nk + kt) % C::kKStages) * C::kKBytes) >> 4);
+          // the two K tiles' MMAs alternate: each waits for its own accumulator's last step
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              tc::mma_ss(tmem + bf * C::kBufCols + kt * kNQ, kd + tc::koff(k, C::kKChunk), qd + tc::koff(k, C::kQChunk),
-                         idesc, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t q = khi_q | (ql + (uint32_t)tc::koff(k, C::kQChunk));
+            const uint32_t ko = (uint32_t)tc::koff(k, (uint32_t)a.k_chunk);
+            tc::mma_ss(col, khi | (kl0 + ko), q, idesc, k > 0 ? 1u : 0u);
+            if (two) tc::mma_ss(col + kNQ, khi | (kl1 + ko), q, idesc, k > 0 ? 1u : 0u);
           }
           tc::commit(bar(C::bS + bf));
           tc::commit(bar(C::bQEmpty + st));
@@ -387,8 +412,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         int ps[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          const int h = hb * a.H + hn[e], i = (u.pb_lo + pb) * a.P + pn[e];
-          const bool in = hn[e] < a.H && h < a.r && i < a.S_q;
+          int h = hb * a.H + hn[e], i = (u.pb_lo + pb) * a.P + pn[e];
+          bool in = hn[e] < a.H && h < a.r && i < a.S_q;
+          if (a.flat) {
+            const int x = t * kNQ + e * 32 + lane;
+            h = a.div_P.div(x);  // P = S_q
+            i = x - h * a.S_q;
+            in = h < a.r;
+          }
           l[e] = in ? __ldg(a.lse + ((long long)u.b * a.h_q + u.g * a.r + h) * a.S_q + i) : -INFINITY;
           ps[e] = a.causal ? (int)min((long long)u.qs + i, (long long)kFar) : kFar;
         }
@@ -448,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const float2 c2 = make_float2(a.sl2, a.sl2);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
-          const int c0 = ch * 64 + cc * 32;
+          const int c0 = cc * 64 + ch * 32;
           const int lo = crange(bf)[c0 / 16], hi = crange(bf)[c0 / 16 + 1];
           if (hi < k0 || k0 >= u.kv) continue;  // no column sees one of the keys, or there are none
           float s[32];
@@ -642,11 +673,7 @@ __global__ void __launch_bounds__(SCfg<D, MT>::kThreads, 1)
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      if (lane < n_sub) {
-#pragma unroll
-        for (int ch = 0; ch < C::kNch; ++ch)
-          tma_load_2d(base + st * C::kStage + ch * C::kKChunk + lane * a.sub * 128, &tmk, full(st), ch * 64, row);
-      }
+      if (lane < n_sub) load_keys<C::kNch>(a, base + st * C::kStage, &tmk, full(st), lane, row);
       if (lane < C::kRows) {
         // a row without a finite lse (no visible key, padding) takes part in nothing
         const bool in = l != -INFINITY && l == l;
@@ -706,7 +733,7 @@ __global__ void __launch_bounds__(SCfg<D, MT>::kThreads, 1)
       for (int ks = 0; ks < D / 16; ++ks) {
         const int d8k = ks * 2 + ((lane >> 3) & 1), d8q = ks * 2 + (qi >> 1);
         uint32_t b0, b1, b2, b3;
-        ldsm_x4(swz128(kb + (d8k >> 3) * C::kKChunk, krow, d8k & 7), b0, b1, b2, b3);
+        ldsm_x4(swz128(kb + (krow >> 3) * a.k_group + (d8k >> 3) * a.k_chunk, krow & 7, d8k & 7), b0, b1, b2, b3);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           uint32_t qf[4];
@@ -853,7 +880,7 @@ __global__ void __launch_bounds__(128) kv_weights_fp32_kernel(WArgs a, const flo
 // -------------------------------------------------------------------------------------------------
 // Tile geometry: P = min(S_q, 128) positions of as many heads as fit (small: all rows of the group).
 struct Geometry {
-  bool small;
+  bool small, flat;
   int keys;  // of a unit
   int P, H, N, hblocks, npb, parts;
 };
@@ -868,6 +895,8 @@ Geometry geometry(int B, int h_q, int h_kv, int S_q, int T_max, int num_sms) {
   m.keys = m.small ? kBK : Cfg<64>::kKeys;
   m.N = (m.P * m.H + 15) / 16 * 16;
   m.hblocks = (r + m.H - 1) / m.H;
+  m.flat = !m.small && S_q < 128;
+  if (m.flat) m.hblocks = (int)(((long long)r * S_q + 127) / 128);
   m.npb = (S_q + m.P - 1) / m.P;
   m.parts = 1;
   const long long units = (long long)B * h_kv * ((T_max + m.keys - 1) / m.keys);
@@ -925,6 +954,7 @@ WArgs make_args(const KvWeightsArgs& a, const Geometry& m) {
   w.hblocks = m.hblocks;
   w.npb = m.npb;
   w.N = m.N;
+  w.flat = m.flat ? 1 : 0;
   w.nkt = (a.T_max + m.keys - 1) / m.keys;
   w.part_keys = w.nkt * m.keys;
   w.parts = m.parts;
@@ -944,17 +974,22 @@ WArgs make_args(const KvWeightsArgs& a, const Geometry& m) {
   w.page_size = a.page_size;
   w.num_pages = a.num_pages;
   w.sub = kv_weights_sub(a.block_table != nullptr, a.page_size);
+  w.k_4d = kv_weights_4d(a.block_table != nullptr, a.d_h) ? 1 : 0;
+  w.k_chunk = w.k_4d ? 1024 : kBK * 128;
+  w.k_group = w.k_4d ? 2048 : 1024;
   w.err = a.err;
   return w;
 }
 
 }  // namespace kw
 
+bool kv_weights_4d(bool paged, int d_h) { return paged && d_h == 128; }
+
 int kv_weights_sub(bool paged, int page_size) { return !paged ? 128 : page_size % 64 == 0 ? 64 : 16; }
 
 KvWeightsTile kv_weights_tile(int h_q, int h_kv, int S_q) {
   const kw::Geometry m = kw::geometry(1, h_q, h_kv, S_q, 1, 0);
-  return {m.small, m.P, m.H, S_q * (h_q / h_kv) > 16 ? 32 : 16};
+  return {m.small, m.flat, m.P, m.H, S_q * (h_q / h_kv) > 16 ? 32 : 16};
 }
 
 size_t kv_weights_workspace_bytes(int B, int h_q, int h_kv, int S_q, int T_max, gqa_dtype dtype, int num_sms) {
