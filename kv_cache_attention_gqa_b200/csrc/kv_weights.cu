@@ -10,13 +10,14 @@
 // the sum over rows runs along the columns a thread reads of its own lane: no exchange between threads, no
 // atomics, the same result every time. A Q tile is 128 columns: positions of one head, or with
 // fewer than 128 positions the rows of the group's heads end to end.
-// Bound by the exponentials (one per visible pair, 16 a clock and SM: 2048 clocks per 256 x 128 tile) and
-// the MMAs, which run at 1650 clocks per tile instead of 1024 because both operands come from shared memory
-// and fill its 128 bytes a clock by themselves. Four warpgroups: one per 128 keys and half of the columns;
-// S^T is buffered twice. Measured (B200): 32 heads over 8 KV heads, 4096 rows, causal, d = 128: 116 us, 590
-// TFLOP/s. Even tiles to two warpgroups and odd ones to the other two: 137 us (each pair waits for its only
-// buffer's MMA); a quarter to a half of the exponentials as polynomials on the multiply-add pipe: no gain;
-// 128 keys a unit: 109 to 150 us for twice the L2 reads of Q.
+// Four warpgroups: one per 128 keys and half of the columns; S^T is buffered twice. Bound by the exponentials (one
+// per visible pair, 16 a clock and SM: 2048 of the 3300 clocks a 256 x 128 tile takes; the rest is TMEM loads and
+// waits between the roles). Measured (B200, d = 128): 32 heads over 8 KV heads, 4096 rows, causal: 111 us, 617
+// TFLOP/s; 33 rows over 2 x 32768 ragged keys in 16-key pages: 51 us. What did not help, at 4096 rows (best
+// other form 115 us): even tiles to two warpgroups and odd ones to the other two, 137 us (each pair waits for its
+// only buffer's MMA); a quarter, a half, three quarters of the exponentials as polynomials on the multiply-add
+// pipe, 115, 124, 141 us; K as the A operand from TMEM with three 128-column score tiles, 126 us; 128 keys a
+// unit, 109 us before the other steps, for twice the L2 reads of Q.
 // When the units are fewer than the SMs need, or uneven (causal), the query rows of a unit are cut into
 // `parts`, whose sums meet in a second launch in a fixed order.
 // The grid is persistent, one CTA per SM; all roles walk the same units:
@@ -72,8 +73,8 @@ struct WArgs {
   int max_pages, page_size, num_pages, sub;  // sub: keys per K copy (128, or 64 / 16 on a paged cache)
   // Where a K tile's rows lie in shared memory: `k_chunk` bytes between its 64-column chunks, `k_group` between
   // groups of 8 rows. Plane by plane (16384, 1024), or on a paged cache with d = 128 both chunks of a group side by
-  // side (1024, 2048): the copy of a sub-tile is then one box of four dimensions instead of one per chunk
-  // (16 copies of 2 KB a tile were the bound of paged calls: 54 us for the case below).
+  // side (1024, 2048): the copy of a sub-tile is then one box of four dimensions instead of one per chunk (33 rows
+  // over paged keys 54 -> 51 us).
   int k_chunk, k_group, k_4d;
   unsigned* err;
 };
