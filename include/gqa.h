@@ -422,7 +422,8 @@ gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_
  * queries and the lse of a forward call (gqa_prefill, gqa_decode, gqa_decode_paged):
  *   weights[b, g, j] (+)= sum over the heads a of group g and the rows i that see key j of
  *                         exp(scale q[b, a, i] . k[b, g, j] - lse[b, a, i]).
- * Summed over j this gives r S_q (each row's softmax sums to one). It is what kv_evict ranks keys by.
+ * Summed over j this gives r S_q (each row's softmax sums to one). It is what kv_evict ranks keys by. The scores are
+ * plain ones: without a cap, a bias or key ranges.
  *
  *   q          (B, h_q, S_q, d_h) position-encoded queries; S_q = 1 for a decoded token.
  *   k_cache    (B, h_kv, T_max, d_h), or the page pool (num_pages, h_kv, page_size, d_h) with its
