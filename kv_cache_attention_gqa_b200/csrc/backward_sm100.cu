@@ -950,7 +950,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         if (a.mod.range) {
           const int2 rg = a.mod.range[(long long)t.b * a.S_q + qi];
           k_first = max(k_first, rg.x);
-          k_last = min(k_last, rg.y - 1);
+          k_last = min(k_last, max(rg.y, 0) - 1);
         }
         if (a.mod.slopes) slope2 = a.mod.slopes[t.g * a.r + t.hb * a.H + h] * kLog2e;
       }
@@ -1015,6 +1015,8 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         const bool before = a.causal || key0 + 31 <= t.pos_min, after = key0 >= t.pos_max;
         const bool one = before || after;
         const float step = before ? slope2 : -slope2, from = step * away - lse2;
+        // kMod: which of the half's 32 keys this row sees
+        const uint32_t sees = bits_between(k_first - key0, k_last - key0 + 1);
         auto columns = [&](auto kBias, auto kMask) {
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -1032,7 +1034,10 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
               const float2 tt = make_float2(sf[x], sf[x + 1]);
               ds = mul2(ds, fma2(make_float2(-tt.x, -tt.y), tt, make_float2(1.f, 1.f)));
             }
-            if (kMod ? kMask.value != 0 : need_mask) {
+            if constexpr (kMod && kMask.value) {
+              if (!(sees >> x & 1u)) ds.x = 0.f;
+              if (!(sees >> (x + 1) & 1u)) ds.y = 0.f;
+            } else if (!kMod && need_mask) {
               if (key0 + x < k_first || key0 + x > k_last) ds.x = 0.f;
               if (key0 + x + 1 < k_first || key0 + x + 1 > k_last) ds.y = 0.f;
             }

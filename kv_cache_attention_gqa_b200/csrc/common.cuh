@@ -230,6 +230,15 @@ __device__ __forceinline__ float mod_score(float dot, float scale, float cap, fl
   return slope != 0.f ? fmaf(-slope, fabsf((float)away), s) : s;
 }
 
+// Bits [lo, hi) of 32, the bounds clamped to them. A test of one bit costs an instruction, where two bounds cost two
+// comparisons.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  uint32_t a, b;  // shl.b32 by 32 or more gives 0
+  asm("shl.b32 %0, %1, %2;" : "=r"(a) : "r"(0xffffffffu), "r"(max(lo, 0)));
+  asm("shl.b32 %0, %1, %2;" : "=r"(b) : "r"(0xffffffffu), "r"(max(hi, 0)));
+  return a & ~b;
+}
+
 // tanh of a pair with |x| <= kTanhSmall: x times a polynomial in x^2 (least maximum relative error, fitted by
 // iterated reweighting: 7.3e-8; with fp32 rounding 1.8e-7).
 constexpr float kTanhSmall = 0.6f;

@@ -386,13 +386,13 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
     if constexpr (kMod) {
       if (a.window > 0) {
         const long long ml = pos - a.window;
-        win_last = (int)(ml < -1 ? -1 : (ml > 0x7fffffffLL ? 0x7fffffffLL : ml));
+        win_last = (int)(ml < -1 ? -1 : (ml > 0x7ffffffeLL ? 0x7ffffffeLL : ml));  // one more is an int still
       }
       if (store_row) {
         if (a.mod.range) {
           const int2 rg = a.mod.range[(long long)w.b * a.S_q + qi];
           win_last = max(win_last, rg.x > 0 ? rg.x - 1 : -1);
-          key_last = min(key_last, rg.y - 1);
+          key_last = min(key_last, max(rg.y, 0) - 1);
         }
         if (bias) slope2 = a.mod.slopes[w.g * a.r + w.hb * a.H + h] * kLog2e;
       }
@@ -454,11 +454,19 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
           }
         }
       }
-      if (need_mask) {
+      if (kMod && need_mask) {
+        // the bounds are in [-1, 2^31 - 1), so the differences are ints
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t sees = bits_between(win_last - key0 - 32 * q + 1, key_last - key0 - 32 * q + 1);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sr[32 * q + k] = sees >> k & 1u ? sr[32 * q + k] : -INFINITY;
+        }
+      } else if (need_mask) {
 #pragma unroll
         for (int k = 0; k < kBN; ++k) {
           const int key = key0 + k;
-          const bool vis = key <= key_last && (!(kWin || kMod) || key > win_last);
+          const bool vis = key <= key_last && (!kWin || key > win_last);
           sr[k] = vis ? sr[k] : -INFINITY;
         }
       }

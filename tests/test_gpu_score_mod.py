@@ -210,3 +210,32 @@ def test_padded_batch_in_a_captured_step():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want[name])), name
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 40), (False, 0)])
+def test_ranges_at_the_limits_of_an_int(causal, window, dtype):
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S, d = 1, 4, 2, 200, 64
+    least, most = -2 ** 31, 2 ** 31 - 1
+    rows = torch.tensor([[least, most], [0, least], [most, most], [most, least], [5, most], [least, 9], [least, least],
+                         [3, 150]], dtype=torch.int64)
+    rg = rows[torch.arange(S) % len(rows)].to(torch.int32)[None].contiguous()
+    q, k, v = _randn((B, h_q, S, d), dtype, 1), _randn((B, h_kv, S, d), dtype, 2), _randn((B, h_kv, S, d), dtype, 3)
+    up = _randn((B, h_q, S, d), dtype, 4)
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), key_range=rg.numpy(), d_o=up.double(),
+                                        causal=causal, window=window)
+    q, k, v, up, rg = q.cuda(), k.cuda(), v.cuda(), up.cuda(), rg.cuda()
+    how = dict(causal=causal, window=window, key_range=rg)
+    o, lse = gqa.prefill(q, k, v, return_lse=True, **how)
+    _check(o, lse, ref, dtype, "prefill")
+    for name, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, **how), ref[3:]):
+        assert_grad_close(got.double().cpu().numpy(), want, name, fp32=dtype == torch.float32)
+    for i in range(len(rows)):  # the same range for every head of a step at the end of the cache
+        q1 = q[:, :, -1].contiguous()
+        ro, rl, mag = oracle.modified_attention_ref(q1[:, :, None].double().cpu(), k.double().cpu(), v.double().cpu(),
+                                                    key_range=rg[:, i:i + 1].cpu().numpy(), q_start=[S - 1])[:3]
+        o, lse = gqa.decode(q1, k, v, kv_len=[S], return_lse=True, key_range=rg[:, i].contiguous())
+        _check(o[:, :, None], lse[..., None], (ro, rl, mag), dtype, f"decode {i}")
+    assert gqa.get_device_error() == 0
