@@ -1231,10 +1231,10 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
     if (a.mod.range) {
       const int n_qb = (a.S_q + bw::kKvBQ - 1) / bw::kKvBQ;
       int4* hull = reinterpret_cast<int4*>(a.hull);
-      e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, p.n_qt, s);
+      e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, p.n_qt, nullptr, s);
       if (e != cudaSuccess) return e;
       int4* hull64 = hull + (size_t)a.B * p.n_qt;
-      e = launch_row_hull(a.mod.range, hull64, a.B, a.S_q, bw::kKvBQ, n_qb, s);
+      e = launch_row_hull(a.mod.range, hull64, a.B, a.S_q, bw::kKvBQ, n_qb, nullptr, s);
       if (e != cudaSuccess) return e;
       p.mod.hull = hull;
       p.hull64 = hull64;

@@ -20,7 +20,9 @@ struct ScoreMod {
 struct ModArgs;
 ModArgs mod_args(const ScoreMod& m, float scale);  // without the hull
 // per (sequence, block of `rows` query rows): ModArgs::hull; n_blocks = ceil(S_q / rows)
-cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks, cudaStream_t s);
+// ticket: a counter that the launch sets to 0, or null
+cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks, int* ticket,
+                            cudaStream_t s);
 
 struct AppendArgs {
   void* k_cache;
@@ -133,7 +135,7 @@ struct PrefillArgs {
   int expire_wait = 0;  // test hook (gqa_debug_expire_waits): one bounded wait runs out
   unsigned* err;
   ScoreMod mod;
-  void* workspace = nullptr;  // bf16 with key ranges: the tiles' hulls
+  void* workspace = nullptr;  // bf16 with key ranges: the tiles' hulls, then a ticket counter
 };
 // fp32 check mode (scalar FFMA)
 cudaError_t launch_prefill_fp32(const PrefillArgs& a, cudaStream_t s);

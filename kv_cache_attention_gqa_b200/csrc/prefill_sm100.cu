@@ -119,6 +119,7 @@ struct PArgs {
   int window;  // 0: none; W > 0: row at position p also needs key j > p - W (causal only)
   int expire_wait;  // test hook: CTA 0's producer first waits on a barrier that nothing signals
   unsigned* err;
+  int* ticket;  // kMod, pair mode with key ranges: items handed out past the first gridDim.x (null: the snake)
   ModArgs mod;  // kMod kernels only; mod.hull has an entry per sequence and tile of P positions
 };
 
@@ -143,10 +144,13 @@ enum : int {
                                                 //   halfway through that round (128 arrivals)
   kBarQEmpty = kBarTurn + 5,               // + chain: the chain's last S = Q K^T of an item
                                                 //   completed (its Q rows may be replaced)
-  kNumBars = kBarQEmpty + kTiles
+  kBarItem = kBarQEmpty + kTiles,          // + slot: an item number is in the slot
+  kBarItemRead = kBarItem + 4,             // + slot: the issuers and the softmax warps have read it
+  kNumBars = kBarItemRead + 4
 };
-// the barriers, then the TMEM address, the abort flag and the split-mode merge's abort word
-static_assert(kNumBars * 8 + 12 <= kBarBytes, "barrier block");
+// the barriers, then the TMEM address, the abort flag, the split-mode merge's abort word and four item slots
+static_assert(kNumBars * 8 + 28 <= kBarBytes, "barrier block");
+constexpr int kItemReaders = 2 + 4 * kTiles;  // warps
 
 // Bounded wait that also gives up as soon as another thread of the CTA has aborted.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort,
@@ -291,6 +295,45 @@ __device__ __forceinline__ long long item_of(int it) {
   return base + ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+// Key ranges leave the items' work uneven in a way the host does not know (documents of a packed row: the snake's
+// busiest CTA had 1.3 times the mean). The producer then draws items from a ticket counter as it gets to them, and
+// passes the numbers on through four slots; every other warp of a role reads them in order, after an abort too.
+struct Items {
+  const PArgs& a;
+  uint64_t* bars;
+  int it;  // items read
+  __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
+  __device__ __forceinline__ volatile int* slot(int i) const {
+    return reinterpret_cast<volatile int*>(bars + kNumBars) + 3 + (i & 3);
+  }
+  // a whole warp's next item; n_items and on: none
+  template <int kMod, bool kSplit>
+  __device__ __forceinline__ long long next(int lane) {
+    const int i = it++;
+    if constexpr (kMod && !kSplit) {
+      if (a.ticket) {
+        volatile int no_abort = 0;
+        const bool got = __all_sync(
+            0xffffffffu, wait_bar(bar(kBarItem + (i & 3)), (uint32_t)((i >> 2) & 1), &no_abort, a.err));
+        const int item = got ? *slot(i) : a.n_items;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarItemRead + (i & 3)));
+        return item;
+      }
+    }
+    return item_of(i);
+  }
+  // the producer hands on the CTA's i-th item; false: the slot's last one was never read
+  __device__ __forceinline__ bool hand_on(int i, int item) {
+    volatile int no_abort = 0;
+    if (i >= 4 && !wait_bar(bar(kBarItemRead + (i & 3)), (uint32_t)(((i >> 2) - 1) & 1), &no_abort, a.err))
+      return false;
+    *slot(i) = item;
+    mbar_arrive(bar(kBarItem + (i & 3)));
+    return true;
+  }
+};
+
 // Running counts over the items a CTA has done so far. Every role derives them from the same
 // items, so each role knows the phase of every barrier it waits on.
 struct Seq {
@@ -356,8 +399,9 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
   // false once a wait gave up (the error word says so): this chain's rows of the remaining items
   // are written as zeros with lse = -inf, without touching TMEM
   bool ok = true;
+  Items items = {a, bars, 0};
   for (int it = 0; !kSplit || it < 1; ++it) {  // split mode: one item per CTA
-    const long long item = item_of(it);
+    const long long item = items.next<kMod, kSplit>(lane);
     if (item >= a.n_items) break;
     const Work w = make_work<kMod>(a, (int)item);
     const int J0 = cJ, I0 = cI, T0 = cT, A0 = cA;  // counts before this item
@@ -743,8 +787,10 @@ __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, u
   };
   Seq sq = {};
   bool ok = true;
+  Items items = {a, bars, 0};
+  const int lane = threadIdx.x & 31;
   for (int it = 0; ok && (!kSplit || it < 1); ++it) {  // split mode: one item per CTA
-    const long long item = item_of(it);
+    const long long item = items.next<kMod, kSplit>(lane);
     if (item >= a.n_items) break;
     const Work w = make_work<kMod>(a, (int)item);
     const Seq s0 = sq;
@@ -795,6 +841,10 @@ __device__ __forceinline__ void mma_role(const PArgs& a, int t, uint32_t tmem, u
     }
     if constexpr (!kSplit) pass_over(nb, w.nbmax);
   }
+  // after an abort the item numbers are still read, so that the producer can hand them on to the softmax
+  if (kMod && !kSplit && a.ticket && !ok)
+    while (items.next<kMod, kSplit>(lane) < a.n_items) {
+    }
   // every MMA issued above has completed before TMEM is released
   if (elect_one()) tc::commit(bar(kBarDone + t));
   __syncwarp();
@@ -837,6 +887,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < kTiles; ++t) mbar_init(bar(kBarDone + t), 1);
     for (int i = 0; i < 5; ++i) mbar_init(bar(kBarTurn + i), 128);
     mbar_init(bar(kBarNever), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kBarItem + i), 1);
+      mbar_init(bar(kBarItemRead + i), kItemReaders);
+    }
     *abort = 0;
     *xabort = 0;
     fence_barrier_init();
@@ -869,6 +923,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Test hook (off unless the host enabled it): CTA 0 first waits on a barrier that nothing
     // signals, so its bounded wait runs out, records GQA_DEVERR_TIMEOUT and aborts the CTA before
     // any copy is issued; every other role then gives up through the abort flag.
+    const bool drawn = kMod && !kSplit && a.ticket;  // items come from the ticket counter
+    Items items = {a, bars, 0};
+    int next = 0, handed = 0;  // the item after this one; items handed on
+    if (drawn) {
+      next = blockIdx.x;
+      items.hand_on(handed++, next);
+    }
     bool ok = !(a.expire_wait && blockIdx.x == 0) || wait_bar(bar(kBarNever), 0, abort, a.err);
     // wait for the readers `rd` (2 bits) of a stage on their empty barriers empty0 + chain * n + s
     auto release = [&](uint32_t rd, uint32_t& ph, int empty0, int n, int s) {
@@ -882,8 +943,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Seq sq = {};
     for (int it = 0; ok && (!kSplit || it < 1); ++it) {  // split mode: one item per CTA
-      const long long item = item_of(it);
+      const long long item = drawn ? next : item_of(it);
       if (item >= a.n_items) break;
+      if (drawn) {
+        next = min((int)gridDim.x + atomicAdd(a.ticket, 1), a.n_items);
+        if (!(ok = items.hand_on(handed++, next))) break;
+      }
       const Work w = make_work<kMod>(a, (int)item);
       const Seq s0 = sq;
       advance(sq, w);
@@ -932,6 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nv;
       }
     }
+    if (drawn && !ok && next < a.n_items) items.hand_on(handed, a.n_items);  // no more: others draw the rest
     // Drain (bounded, whatever the abort state): no copy may still be landing in shared memory
     // when the CTA exits.
     volatile int no_abort = 0;
@@ -1011,6 +1077,7 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
   p.window = a.window;
   p.expire_wait = a.expire_wait;
   p.err = a.err;
+  p.ticket = nullptr;
   const long long items = (long long)(p.split ? n_qt : p.n_pairs) * units;
   if (items <= 0) return cudaSuccess;
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -1026,7 +1093,9 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
     p.mod = mod_args(a.mod, a.scale);
     if (a.mod.range) {
       int4* hull = reinterpret_cast<int4*>(a.workspace);
-      const cudaError_t e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, n_qt, s);
+      int* ticket = reinterpret_cast<int*>(hull + (size_t)a.B * n_qt);
+      if (!p.split) p.ticket = ticket;
+      const cudaError_t e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, n_qt, p.ticket, s);
       if (e != cudaSuccess) return e;
       p.mod.hull = hull;
     }
@@ -1064,7 +1133,7 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
 
 size_t prefill_hull_bytes(int B, int h_q, int h_kv, int S_q) {
   const int P = pf::kBM / prefill_heads_per_tile(h_q, h_kv);
-  return (size_t)((S_q + P - 1) / P) * B * sizeof(int4);
+  return (size_t)((S_q + P - 1) / P) * B * sizeof(int4) + sizeof(int4);
 }
 
 int prefill_heads_per_tile(int h_q, int h_kv) {

@@ -21,9 +21,11 @@ namespace {
 
 // One warp per block of `rows` query rows of one sequence. x, y: the least lo and the largest hi of the rows
 // that see any key (y = 0: none does); z, w: the largest lo and the least hi of all of them, so that keys
-// z <= j < w are in every row's range (a row without a key makes that empty).
+// z <= j < w are in every row's range (a row without a key makes that empty). Resets the ticket counter of the kernel
+// that follows, where it has one.
 __global__ void __launch_bounds__(256) row_hull_kernel(const int2* range, int4* hull, int B, int S_q, int rows,
-                                                       int n_blocks) {
+                                                       int n_blocks, int* ticket) {
+  if (ticket && blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
   const long long wid = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (wid >= (long long)B * n_blocks) return;
@@ -52,10 +54,11 @@ __global__ void __launch_bounds__(256) row_hull_kernel(const int2* range, int4* 
 }  // namespace
 
 cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks,
-                            cudaStream_t s) {
+                            int* ticket, cudaStream_t s) {
   const long long warps = (long long)B * n_blocks;
   row_hull_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(reinterpret_cast<const int2*>(range),
-                                                              reinterpret_cast<int4*>(hull), B, S_q, rows, n_blocks);
+                                                              reinterpret_cast<int4*>(hull), B, S_q, rows, n_blocks,
+                                                              ticket);
   return cudaGetLastError();
 }
 
