@@ -324,8 +324,8 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * mod NULL, or nothing set in it: the plain call, bit for bit.
  * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
  * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. gqa_prefill_backward_mod needs
- * gqa_prefill_backward_mod_workspace_size bytes with a key_range, gqa_prefill_backward's without. The
- * decode calls take gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is
+ * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in bf16 it
+ * takes rowsum(dO o) from the probabilities, in fp32, and does not read o. The decode calls take gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is
  * negative, NaN or infinite.
  */
 typedef struct {

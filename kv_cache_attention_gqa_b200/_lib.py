@@ -488,7 +488,7 @@ def prefill_backward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     scale = _scale(scale)
     mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, S_q, 2))
-    need = (_lib.gqa_prefill_backward_workspace_size(B, h_q, S_q) if key_range is None
+    need = (_lib.gqa_prefill_backward_workspace_size(B, h_q, S_q) if mod is None
             else _lib.gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q))
     if ws is None or _ws_bytes(ws) < need:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)

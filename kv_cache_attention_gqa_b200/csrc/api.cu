@@ -543,7 +543,9 @@ gqa_status gqa_prefill_backward(const void* q, const void* k_cache, const void* 
 
 size_t gqa_prefill_backward_mod_workspace_size(int B, int h_q, int h_kv, int S_q) {
   if (B <= 0 || h_q <= 0 || h_kv <= 0 || S_q <= 0 || h_q % h_kv != 0) return 0;
-  return gqa_prefill_backward_workspace_size(B, h_q, S_q) + (backward_hull_bytes(B, h_q, h_kv, S_q) + 255) / 256 * 256;
+  const size_t rows = (size_t)B * h_q * S_q;  // the second part of D
+  return gqa_prefill_backward_workspace_size(B, h_q, S_q) + (rows * 4 + 255) / 256 * 256 +
+         (backward_hull_bytes(B, h_q, h_kv, S_q) + 255) / 256 * 256;
 }
 
 gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const void* v_cache, const void* o,
@@ -566,7 +568,7 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
     return GQA_ERR_UNSUPPORTED;
   if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
   const size_t base = gqa_prefill_backward_workspace_size(B, h_q, S_q);
-  const size_t need = mod && mod->key_range ? gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q) : base;
+  const size_t need = score_mod(mod).on() ? gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q) : base;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
     return GQA_ERR_WORKSPACE;
   BackwardArgs a;
@@ -595,7 +597,8 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
   a.drow = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + half);
   a.ticket = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(workspace) + 2 * half);
   a.mod = score_mod(mod);
-  a.hull = reinterpret_cast<uint8_t*>(workspace) + base;
+  a.dpart1 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + base);
+  a.hull = reinterpret_cast<uint8_t*>(workspace) + base + half;
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -8,7 +8,7 @@
 //   dS = P * (dP - D),  dQ_a = scale dS K_g,  dK_g += scale dS^T Q_a.
 // The mask is the forward's: causal by absolute position, length, and an optional sliding window.
 //
-// Two launches: rowterm, then one persistent grid (one CTA per SM) whose CTAs take work items in
+// Two launches (with modified scores three and their hulls): rowterm, then one persistent grid (one CTA per SM) whose CTAs take work items in
 // the order dkdv tiles (heaviest first), then dq tiles (heaviest first): item c for CTA c, then
 // items from a ticket counter that rowterm resets, so an SM that finishes early takes the next
 // item, as the hardware's CTA scheduler would, without a CTA exit and launch per item (measured:
@@ -31,7 +31,10 @@
 //               S = Q K^T, dP = dO V^T (A = the tile's Q / dO rows, copied once into TMEM;
 //               B = K / V from shared memory), then dS -> bf16 into TMEM, dQ += dS K (A = dS from
 //               TMEM, B = K, MN-major view).
-// kMod kernels (modified scores): P comes from the capped and biased score and dS gains the cap's derivative
+// kMod kernels (modified scores): D is taken as rowsum(P * dP) in fp32, by a run of the dq tiles without the dQ
+// product (row_sums) in front. With peaked scores dS is a small difference of dP and D, and a D from the O that the
+// forward rounded to bf16 left dQ and dK with 2.3 times the error of rounding them (0.0039 against 0.0017 of the
+// norm; 0.0024 with this D). P comes from the capped and biased score and dS gains the cap's derivative
 // 1 - tanh^2; the query blocks of a key tile and the key blocks of a dq tile follow the rows' key ranges, whose
 // hulls per row block two small kernels in front work out (row_hull).
 // Masks: on blocks that straddle the diagonal, the window or the length, each elementwise thread
@@ -62,7 +65,8 @@ constexpr uint32_t kColAcc0 = 256;  // first accumulator column (scores and thei
 
 struct BArgs {
   const float* lse2;  // (B*h_q*S_q) base-2 log-sum-exp per row (+inf for a row with no key)
-  const float* drow;  // (B*h_q*S_q) D = rowsum(dO * O)
+  const float* drow;  // (B*h_q*S_q) D = rowsum(dO * O); kMod: rowsum(P * dP), the even halves' share
+  float* dpart[2];    // kMod: drow (to write) and the odd halves' share
   void* dq;
   void* dk;
   void* dv;
@@ -75,7 +79,7 @@ struct BArgs {
   int causal, window;
   FastDiv div_per, div_gh, div_hb;  // by B*h_kv*hblocks, h_kv*hblocks, hblocks (dq tile numbers)
   int n_items;              // dkdv tiles + dq tiles
-  int* ticket;              // items handed out past the first gridDim.x (reset by rowterm)
+  int* ticket;              // items handed out past the first gridDim.x (reset by rowterm or row_start)
   unsigned* err;
   ModArgs mod;              // kMod kernels only; mod.hull: of the dq tiles
   const int4* hull64;       // kMod with ranges: of the 64-row query blocks (dkdv)
@@ -382,7 +386,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
         const int qi = qb * kKvBQ + c;
         const long long row = (long long)z * a.S_q + qi;
         sl[c] = qi < a.S_q ? -a.lse2[row] : -INFINITY;  // stored negated for the fused FMAs
-        sl[kKvBQ + c] = qi < a.S_q ? -a.drow[row] : 0.f;
+        sl[kKvBQ + c] = qi >= a.S_q ? 0.f : kMod ? -(a.drow[row] + a.dpart[1][row]) : -a.drow[row];
         if (kMod && a.mod.range) {
           const int2 rg = qi < a.S_q ? a.mod.range[(long long)b * a.S_q + qi] : make_int2(0, 0);
           srange[st * 2 * kKvBQ + c] = rg.x;
@@ -734,7 +738,9 @@ __device__ __forceinline__ DqTile dq_tile(const BArgs& a, int tile) {
 // which overwrites the accumulator, waits for dS that those warps produce after reading it out.
 // The producer hands each tile's number to the other roles through `s_items` (two slots), and a
 // number past the last item ends the run.
-template <int D, bool kMod>
+// kSum: the same walk without dS and dQ; each elementwise thread adds up P * dP of its row and its half of every block,
+// and the halves' sums go to dpart. (n_dkdv is 0, and the ticket counter another one.)
+template <int D, bool kMod, bool kSum>
 __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap& tmdo,
                                        const CUtensorMap& tmk, const CUtensorMap& tmv, const BArgs& a,
                                        int item0, int n_dkdv, uint32_t tmem, volatile int* s_items) {
@@ -873,7 +879,9 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
           if (!(ok = wait(kQP + bf, (uint32_t)((jg >> 1) & 1)))) break;
           tc::fence_after_sync();
           const uint64_t dk_mn = tc::smem_desc(sK(st), C::kKChunk, 1024);
-          if (elect_one()) {
+          if (kSum) {  // kQP says that the block's scores were read, so its S and dP are complete
+            if (elect_one()) mbar_arrive(bar(kQKvEmpty + st));
+          } else if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kQBK / 16; ++kk)
               tc::mma_ts(tmem + kColAcc0, tmem + (uint32_t)(64 * bf + (kk >> 1) * 32 + (kk & 1) * 8),
@@ -883,7 +891,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
           __syncwarp();
         }
         if (!ok) break;
-        if (elect_one()) tc::commit(bar(kQDone));  // this tile's dQ is complete
+        if (!kSum && elect_one()) tc::commit(bar(kQDone));  // this tile's dQ is complete
         __syncwarp();
       }
       J += t.nb;
@@ -939,7 +947,8 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       const long long srow = ((long long)t.b * a.h_q + t.g * a.r + t.hb * a.H + h) * a.S_q + qi;
       const long long pos = (long long)t.qs + qi;
       const float lse2 = store_row ? a.lse2[srow] : INFINITY;
-      const float dr = store_row ? a.drow[srow] : 0.f;
+      const float dr = kSum || !store_row ? 0.f : kMod ? a.drow[srow] + a.dpart[1][srow] : a.drow[srow];
+      float2 sum = make_float2(0.f, 0.f);  // kSum
       // keys [k_first, k_last] this row sees (length, causal and window limits as 32-bit bounds)
       const long long kl = a.causal && pos < t.kv - 1 ? pos : (long long)t.kv - 1;
       int k_last = (int)kl;
@@ -978,7 +987,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       mbar_arrive(bar(kQT));
       mbar_arrive(bar(kQdQEmpty));
       // the previous tile's dQ (the MMA warp can start this tile's scores meanwhile)
-      if (prev) {
+      if (!kSum && prev) {
         bool have = prev_blocks && ok;
         if (have) {
           have = wait_bar(bar(kQDone), (uint32_t)((nd - 1) & 1), abort, a.err);
@@ -1030,7 +1039,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
             const float2 arg = fma2(make_float2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1])), c2, nb);
             const float2 pr = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
             float2 ds = mul2(pr, add2(make_float2(__uint_as_float(dv[x]), __uint_as_float(dv[x + 1])), nd2));
-            if (cap) {
+            if (!kSum && cap) {
               const float2 tt = make_float2(sf[x], sf[x + 1]);
               ds = mul2(ds, fma2(make_float2(-tt.x, -tt.y), tt, make_float2(1.f, 1.f)));
             }
@@ -1041,7 +1050,8 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
               if (key0 + x < k_first || key0 + x > k_last) ds.x = 0.f;
               if (key0 + x + 1 < k_first || key0 + x + 1 > k_last) ds.y = 0.f;
             }
-            pd[x / 2] = pack_bf16x2(ds.x, ds.y);
+            if constexpr (kSum) sum = add2(sum, ds);
+            else pd[x / 2] = pack_bf16x2(ds.x, ds.y);
           }
         };
         if constexpr (!kMod) {
@@ -1054,6 +1064,11 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
           if (!bias) columns(Int<0>(), Int<0>());
           else if (one) columns(Int<1>(), Int<0>());
           else columns(Int<2>(), Int<0>());
+        }
+        if constexpr (kSum) {
+          tc::fence_before_sync();
+          mbar_arrive(bar(kQP + bf));
+          continue;
         }
         tc::st16(lane_addr + 64 * bf + 32 * half, pd);  // dS over this half's first columns of S
         // K rows no row of the tile may see (past kv_len: last block; below every row's window:
@@ -1078,6 +1093,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         tc::fence_before_sync();
         mbar_arrive(bar(kQP + bf));
       }
+      if (kSum && store_row) a.dpart[half][srow] = sum.x + sum.y;
       prev = true;
       prev_blocks = t.nb > 0;
       prev_store = store_row;
@@ -1086,7 +1102,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
       J += t.nb;
       ++n;
     }
-    if (prev) {  // the last tile's dQ
+    if (!kSum && prev) {  // the last tile's dQ
       bool have = prev_blocks && ok;
       if (have) {
         have = wait_bar(bar(kQDone), (uint32_t)((nd - 1) & 1), abort, a.err);
@@ -1134,7 +1150,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   const uint32_t tmem = s_tmem;
   for (int item = blockIdx.x; item < a.n_items;) {
     if (item >= n_dkdv) {  // tickets only grow: every later item of this CTA is a dq tile too
-      dq_run<D, kMod>(tmq_tile, tmdo_tile, tmk64, tmv64, a, item, n_dkdv, tmem, s_items);
+      dq_run<D, kMod, false>(tmq_tile, tmdo_tile, tmk64, tmv64, a, item, n_dkdv, tmem, s_items);
       break;
     }
     // the next item's ticket, fetched while this item runs by a thread of the elementwise warps
@@ -1152,6 +1168,43 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
 }
 
+// D = rowsum(P * dP) of modified scores (dpart), over the dq tiles
+template <int D>
+__global__ void __launch_bounds__(kQThreads, 1)
+    row_sums_kernel(const __grid_constant__ CUtensorMap tmq_tile, const __grid_constant__ CUtensorMap tmdo_tile,
+                    const __grid_constant__ CUtensorMap tmk64, const __grid_constant__ CUtensorMap tmv64, BArgs a) {
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_items[2];
+  const int warp = threadIdx.x >> 5;
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  cta_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  dq_run<D, true, true>(tmq_tile, tmdo_tile, tmk64, tmv64, a, blockIdx.x, 0, tmem, s_items);
+  tc::fence_before_sync();
+  cta_sync();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// In front of it, for modified scores: the base-2 lse, zeros for the sums of rows that a run that gave up leaves
+// out, and the two ticket counters.
+__global__ void __launch_bounds__(256) row_start_kernel(const float* lse, float* lse2, float* d0, float* d1,
+                                                        long long rows, int* tickets) {
+  const long long row = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (row < 2) tickets[row] = 0;
+  if (row >= rows) return;
+  const float l = lse[row];
+  lse2[row] = l == -INFINITY || l != l ? INFINITY : l * kLog2e;
+  d0[row] = d1[row] = 0.f;
+}
+
 template <int D, bool kMod>
 cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
@@ -1161,6 +1214,10 @@ cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cud
   if (dev < 0 || dev >= 64 || !attr_set[dev]) {
     e = cudaFuncSetAttribute(backward_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
+    if constexpr (kMod) {
+      e = cudaFuncSetAttribute(row_sums_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, QCfg<D>::kSmem);
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   const long long n1 = (long long)p.n_kb * p.B * p.h_kv;
@@ -1168,6 +1225,15 @@ cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cud
   if (n1 + n2 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (n1 + n2 <= 0) return cudaSuccess;
   BArgs q = p;
+  if constexpr (kMod) {
+    q.n_items = (int)n2;
+    q.ticket = p.ticket + 1;
+    row_sums_kernel<D><<<(unsigned)(n2 < num_sms ? n2 : num_sms), kQThreads, QCfg<D>::kSmem, s>>>(tm[4], tm[5], tm[6],
+                                                                                                 tm[7], q);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    q.ticket = p.ticket;
+  }
   q.n_items = (int)(n1 + n2);
   const long long ctas = n1 + n2 < num_sms ? n1 + n2 : num_sms;  // one CTA per SM
   backward_kernel<D, kMod><<<(unsigned)ctas, kKvThreads, BwCfg<D>::kSmem, s>>>(
@@ -1184,7 +1250,10 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
   const auto* ob = reinterpret_cast<const __nv_bfloat16*>(a.o);
   const auto* dob = reinterpret_cast<const __nv_bfloat16*>(a.d_o);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.d_o)) & 15u) == 0;
-  if (vec && a.d_h == 128) {  // 2 rows per warp, 16 per block
+  if (a.mod.on()) {
+    bw::row_start_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.lse, a.lse2, a.drow, a.dpart1, rows,
+                                                                       a.ticket);
+  } else if (vec && a.d_h == 128) {  // 2 rows per warp, 16 per block
     bw::rowterm_vec_kernel<128><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(ob, dob, a.lse, a.lse2, a.drow,
                                                                              rows, a.ticket);
   } else if (vec && a.d_h == 64) {  // 4 rows per warp, 32 per block
@@ -1199,6 +1268,8 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
   bw::BArgs p;
   p.lse2 = a.lse2;
   p.drow = a.drow;
+  p.dpart[0] = a.drow;
+  p.dpart[1] = a.dpart1;
   p.dq = a.dq;
   p.dk = a.dk;
   p.dv = a.dv;

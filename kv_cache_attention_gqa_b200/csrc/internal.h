@@ -164,7 +164,8 @@ struct BackwardArgs {
   int causal, window;
   float* lse2;  // workspace: (B*h_q*S_q) base-2 lse
   float* drow;  // workspace: (B*h_q*S_q) rowsum(dO * O)
-  int* ticket;  // workspace: the bf16 kernel's work-item counter (reset by its row-term kernel)
+  float* dpart1 = nullptr;  // workspace, bf16 with modified scores: (B*h_q*S_q) a part of rowsum(P * dP)
+  int* ticket;  // workspace: the bf16 kernels' two work-item counters (reset by its row-term kernel)
   unsigned* err;
   ScoreMod mod;
   void* hull = nullptr;  // bf16 with key ranges: the hulls of the dQ tiles, then of 64-row query blocks

@@ -6,6 +6,8 @@ the second product (eps / 2 of the weighted |v|); the rest is fp32 (2e-4 of the 
 50 at 3e-7). lse is fp32: 1e-4, and the cap's tanh (3e-7 of the cap). fp32 check mode: 1e-5 of the largest value, as in
 the other check-mode tests. Gradients: the bounds of the plain backward's tests."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -238,4 +240,62 @@ def test_ranges_at_the_limits_of_an_int(causal, window, dtype):
                                                     key_range=rg[:, i:i + 1].cpu().numpy(), q_start=[S - 1])[:3]
         o, lse = gqa.decode(q1, k, v, kv_len=[S], return_lse=True, key_range=rg[:, i].contiguous())
         _check(o[:, :, None], lse[..., None], (ro, rl, mag), dtype, f"decode {i}")
+    assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("how", [dict(alibi=True), dict(softcap=8.0), dict(docs=True)])
+def test_gradients_keep_to_two_roundings(how, d):
+    """Peaked scores (standard deviation 3) make dS = P (dP - D) a small difference. dS is rounded to bf16 once and so
+    are dQ and dK: each rounding is off by at most 2^-8 of the value, uniformly, so by 2^-8 / sqrt(3) in the mean square;
+    two of them by sqrt(2) times that of the gradient's norm."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S = 1, 8, 2, 700
+    mods, cpu = {}, {}
+    if how.get("alibi"):
+        slopes = 2.0 ** (-8.0 * (1 + torch.arange(h_q)) / h_q)
+        mods["alibi_slopes"], cpu["slopes"] = slopes.cuda(), slopes.numpy()
+    if how.get("softcap"):
+        mods["softcap"] = cpu["softcap"] = how["softcap"]
+    if how.get("docs"):
+        rg = torch.tensor([[lo, hi] for lo, hi in ((0, 300), (300, 333), (333, S)) for _ in range(hi - lo)],
+                          dtype=torch.int32)[None].contiguous()
+        mods["key_range"], cpu["key_range"] = rg.cuda(), rg.numpy()
+    q = (3.0 * _randn((B, h_q, S, d), torch.float32, 1)).to(torch.bfloat16)
+    k, v = _randn((B, h_kv, S, d), torch.bfloat16, 2), _randn((B, h_kv, S, d), torch.bfloat16, 3)
+    up = _randn((B, h_q, S, d), torch.bfloat16, 4)
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), d_o=up.double(), causal=True, **cpu)
+    q, k, v, up = q.cuda(), k.cuda(), v.cuda(), up.cuda()
+    o, lse = gqa.prefill(q, k, v, return_lse=True, **mods)
+    grads = gqa.prefill_backward(q, k, v, o, up, lse, **mods)
+    for name, got, want in zip(("dq", "dk"), grads, ref[3:5]):
+        off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
+        assert off <= 2.0 ** -8 * math.sqrt(2 / 3), (name, off)
+    assert gqa.get_device_error() == 0
+
+
+def test_expired_wait_with_drawn_items():
+    """More work than CTAs, so that items are drawn from the counter: the CTA that gives up hands none on to itself, the
+    others draw the rest, and its rows are zeros."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S, d = 1, 32, 8, 2600, 64
+    q, k, v = (_randn((B, h, S, d), torch.bfloat16, i).cuda() for i, h in ((1, h_q), (2, h_kv), (3, h_kv)))
+    rg = torch.tensor([[p // 500 * 500, S] for p in range(S)], dtype=torch.int32)[None].contiguous().cuda()
+    want, want_lse = gqa.prefill(q, k, v, return_lse=True, key_range=rg)
+    assert gqa.get_device_error() == 0
+    gqa.debug_expire_waits(True)
+    try:
+        o, lse = gqa.prefill(q, k, v, out=torch.full_like(q, float("nan")), return_lse=True, key_range=rg)
+        code = gqa.get_device_error()
+    finally:
+        gqa.debug_expire_waits(False)
+    assert code == 4  # GQA_DEVERR_TIMEOUT
+    gone = torch.isneginf(lse)
+    assert 0 < int(gone.sum()) <= 256
+    assert not o[gone].any() and torch.equal(o[~gone], want[~gone]) and torch.equal(lse[~gone], want_lse[~gone])
+    for _ in range(3):
+        o, lse = gqa.prefill(q, k, v, return_lse=True, key_range=rg)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
     assert gqa.get_device_error() == 0
