@@ -317,16 +317,16 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * and the gradients are those of the modified score; slopes are constants (they get no gradient).
  *   key_range  row i of sequence b sees only keys lo <= j < hi, (lo, hi) = key_range[b, i], within what the causal
  *              mask, window and length leave. It writes a document mask (lo, hi the document's rows), a
- *              bidirectional prefix (causal 0, hi the later of p + 1 and the prefix's end), or both. Rows need no order. lo < 0
- *              means 0. A row without a key is written as zeros, lse = -inf, gradients 0, and is no error. K
+ *              bidirectional prefix (causal 0, hi the later of p + 1 and the prefix's end), or both. Rows
+ *              need no order. lo < 0 means 0. A row without a key is written as zeros, lse = -inf, gradients 0, and is no error. K
  *              and V rows outside the keys that a 128-row tile's rows see between them may hold anything.
  *              bf16 prefill and backward work through the blocks between a tile's least and largest key.
  * mod NULL, or nothing set in it: the plain call, bit for bit.
  * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
  * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. gqa_prefill_backward_mod needs
- * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in bf16 it
- * takes rowsum(dO o) from the probabilities, in fp32, and does not read o. The decode calls take gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is
- * negative, NaN or infinite.
+ * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in
+ * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take
+ * gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite.
  */
 typedef struct {
   float softcap;             /* > 0: cap of the scores; 0: none */

@@ -8,8 +8,8 @@
 //   dS = P * (dP - D),  dQ_a = scale dS K_g,  dK_g += scale dS^T Q_a.
 // The mask is the forward's: causal by absolute position, length, and an optional sliding window.
 //
-// Two launches (with modified scores three and their hulls): rowterm, then one persistent grid (one CTA per SM) whose CTAs take work items in
-// the order dkdv tiles (heaviest first), then dq tiles (heaviest first): item c for CTA c, then
+// Two launches (modified scores have more, below): rowterm, then one persistent grid (one CTA per SM) whose CTAs take
+// work items in the order dkdv tiles (heaviest first), then dq tiles (heaviest first): item c for CTA c, then
 // items from a ticket counter that rowterm resets, so an SM that finishes early takes the next
 // item, as the hardware's CTA scheduler would, without a CTA exit and launch per item (measured:
 // the 512-column TMEM release of an exiting CTA took 3.5-5 us after these kernels' epilogues).
@@ -36,7 +36,8 @@
 // forward rounded to bf16 left dQ and dK with 2.3 times the error of rounding them (0.0039 against 0.0017 of the
 // norm; 0.0024 with this D). P comes from the capped and biased score and dS gains the cap's derivative
 // 1 - tanh^2; the query blocks of a key tile and the key blocks of a dq tile follow the rows' key ranges, whose
-// hulls per row block two small kernels in front work out (row_hull).
+// hulls per row block the launch in front works out (row_start), with the base-2 lse, zeros for the sums of rows that
+// a run that gave up leaves out, and the ticket counters.
 // Masks: on blocks that straddle the diagonal, the window or the length, each elementwise thread
 // compares indices with one pair of 32-bit bounds fixed for the block: the query columns that see
 // its key (dkdv) or the keys its row sees (dq).
@@ -1193,18 +1194,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
   }
 }
 
-// In front of it, for modified scores: the base-2 lse, zeros for the sums of rows that a run that gave up leaves
-// out, and the two ticket counters.
-__global__ void __launch_bounds__(256) row_start_kernel(const float* lse, float* lse2, float* d0, float* d1,
-                                                        long long rows, int* tickets) {
-  const long long row = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (row < 2) tickets[row] = 0;
-  if (row >= rows) return;
-  const float l = lse[row];
-  lse2[row] = l == -INFINITY || l != l ? INFINITY : l * kLog2e;
-  d0[row] = d1[row] = 0.f;
-}
-
 template <int D, bool kMod>
 cudaError_t launch_typed(const BArgs& p, const CUtensorMap* tm, int num_sms, cudaStream_t s) {
   static bool attr_set[64] = {false};  // per device: the shared-memory opt-in is set once
@@ -1250,9 +1239,7 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
   const auto* ob = reinterpret_cast<const __nv_bfloat16*>(a.o);
   const auto* dob = reinterpret_cast<const __nv_bfloat16*>(a.d_o);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.d_o)) & 15u) == 0;
-  if (a.mod.on()) {
-    bw::row_start_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.lse, a.lse2, a.drow, a.dpart1, rows,
-                                                                       a.ticket);
+  if (a.mod.on()) {  // launch_row_start, below
   } else if (vec && a.d_h == 128) {  // 2 rows per warp, 16 per block
     bw::rowterm_vec_kernel<128><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(ob, dob, a.lse, a.lse2, a.drow,
                                                                              rows, a.ticket);
@@ -1299,17 +1286,29 @@ cudaError_t launch_backward_bf16(const BackwardArgs& a, const CUtensorMap* tmaps
   p.hull64 = nullptr;
   if (a.mod.on()) {
     p.mod = mod_args(a.mod, a.scale);
+    RowStart rs;
+    rs.B = a.B;
+    rs.S_q = a.S_q;
+    rs.tickets = a.ticket;
+    rs.n_tickets = 2;
+    rs.lse = a.lse;
+    rs.lse2 = a.lse2;
+    rs.d[0] = a.drow;
+    rs.d[1] = a.dpart1;
+    rs.n_rows = rows;
     if (a.mod.range) {
-      const int n_qb = (a.S_q + bw::kKvBQ - 1) / bw::kKvBQ;
-      int4* hull = reinterpret_cast<int4*>(a.hull);
-      e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, p.n_qt, nullptr, s);
-      if (e != cudaSuccess) return e;
-      int4* hull64 = hull + (size_t)a.B * p.n_qt;
-      e = launch_row_hull(a.mod.range, hull64, a.B, a.S_q, bw::kKvBQ, n_qb, nullptr, s);
-      if (e != cudaSuccess) return e;
-      p.mod.hull = hull;
-      p.hull64 = hull64;
+      rs.range = p.mod.range;
+      rs.rows[0] = p.P;
+      rs.blocks[0] = p.n_qt;
+      rs.hull[0] = reinterpret_cast<int4*>(a.hull);
+      rs.rows[1] = bw::kKvBQ;
+      rs.blocks[1] = (a.S_q + bw::kKvBQ - 1) / bw::kKvBQ;
+      rs.hull[1] = rs.hull[0] + (size_t)a.B * p.n_qt;
+      p.mod.hull = rs.hull[0];
+      p.hull64 = rs.hull[1];
     }
+    e = launch_row_start(rs, s);
+    if (e != cudaSuccess) return e;
     if (a.d_h == 128) return bw::launch_typed<128, true>(p, tmaps, num_sms, s);
     if (a.d_h == 64) return bw::launch_typed<64, true>(p, tmaps, num_sms, s);
     return cudaErrorInvalidValue;

@@ -216,7 +216,7 @@ struct ModArgs {
   const float* slopes = nullptr;  // (h_q) natural-log slopes, or none
   const int2* range = nullptr;    // (B, S_q) (decode: (B)) keys lo <= j < hi of each row, or none
   const int4* hull = nullptr;     // per row block: least lo and largest hi of the rows that see any, then
-                                  // largest lo and least hi of all rows (see row_hull)
+                                  // largest lo and least hi of all rows (RowStart)
 };
 
 // Check mode: the score of one pair in natural units, `t` its tanh (for the gradient; 0 without a cap).

@@ -19,10 +19,25 @@ struct ScoreMod {
 };
 struct ModArgs;
 ModArgs mod_args(const ScoreMod& m, float scale);  // without the hull
-// per (sequence, block of `rows` query rows): ModArgs::hull; n_blocks = ceil(S_q / rows)
-// ticket: a counter that the launch sets to 0, or null
-cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks, int* ticket,
-                            cudaStream_t s);
+// What the kernels with modified scores need worked out in front of them.
+struct RowStart {
+  // Hulls of the key ranges, for up to two sizes of row block (blocks = 0: none). Per (sequence, block of `rows` query
+  // rows), blocks = ceil(S_q / rows): x, y the least lo and the largest hi of the rows that see any key (y = 0: none
+  // does); z, w the largest lo and the least hi of all of them, so that keys z <= j < w are in every row's range (a
+  // row without a key makes that empty).
+  const int2* range = nullptr;
+  int B = 0, S_q = 0;
+  int4* hull[2] = {nullptr, nullptr};
+  int rows[2] = {1, 1}, blocks[2] = {0, 0};
+  int* tickets = nullptr;  // counters to set to 0
+  int n_tickets = 0;
+  // n_rows > 0 (backward): the base-2 lse (+inf for a row without a key), and zeros
+  const float* lse = nullptr;
+  float* lse2 = nullptr;
+  float* d[2] = {nullptr, nullptr};
+  long long n_rows = 0;
+};
+cudaError_t launch_row_start(const RowStart& a, cudaStream_t s);
 
 struct AppendArgs {
   void* k_cache;

@@ -3,8 +3,9 @@
 // moved to the front, in their order, in the caller's cache (in place) or into another.
 //
 // Two launches.
-//   select  one CTA, or for long rows a cluster of them, per (sequence, KV head); each keeps its share of the keys. The threshold weight is found by a radix selection over the
-//           weights' bits mapped to unsigned integers of the same order: passes of 11, 11 and 10 bits, each a
+//   select  one CTA, or for long rows a cluster of them, per (sequence, KV head); each keeps its share of the keys.
+//           The threshold weight is found by a radix selection over the weights' bits mapped to unsigned integers
+//           of the same order: passes of 11, 11 and 10 bits, each a
 //           histogram in shared memory and a scan of its counts (with 8 bits the first pass would be the
 //           exponent alone, a handful of bins that every thread of a warp adds to in turn); the weights are
 //           read from DRAM once and kept in shared memory while they fit. The blocks of a cluster read each

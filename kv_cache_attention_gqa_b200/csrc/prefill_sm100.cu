@@ -51,7 +51,7 @@
 // kMod kernels (modified scores): each thread caps its 128 scores by tanh (a polynomial while they are small
 // against the cap, so that the exponential unit keeps to the softmax; see tanh_scores) and adds the distance bias
 // before the maximum, and a row's key range joins its two 32-bit bounds. A tile's blocks run from the least to the
-// largest key its rows see, which a small kernel in front works out per tile (row_hull).
+// largest key its rows see, which a small kernel in front works out per tile (row_start).
 // TMEM columns: tile t holds S_t at [256 t, 256 t + 128) and O_t at [256 t + 128, 256 t + 128 + D).
 
 #include <math.h>
@@ -1095,7 +1095,16 @@ cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, 
       int4* hull = reinterpret_cast<int4*>(a.workspace);
       int* ticket = reinterpret_cast<int*>(hull + (size_t)a.B * n_qt);
       if (!p.split) p.ticket = ticket;
-      const cudaError_t e = launch_row_hull(a.mod.range, hull, a.B, a.S_q, p.P, n_qt, p.ticket, s);
+      RowStart rs;
+      rs.range = p.mod.range;
+      rs.B = a.B;
+      rs.S_q = a.S_q;
+      rs.hull[0] = hull;
+      rs.rows[0] = p.P;
+      rs.blocks[0] = n_qt;
+      rs.tickets = p.ticket;
+      rs.n_tickets = p.ticket ? 1 : 0;
+      const cudaError_t e = launch_row_start(rs, s);
       if (e != cudaSuccess) return e;
       p.mod.hull = hull;
     }

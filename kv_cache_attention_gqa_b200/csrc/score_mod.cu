@@ -1,5 +1,7 @@
 // Host and device pieces shared by the attention kernels with modified scores: the kernel-side arguments
-// and the hulls of key ranges.
+// and the launch in front of them (hulls of key ranges, row terms).
+
+#include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -19,21 +21,32 @@ ModArgs mod_args(const ScoreMod& m, float scale) {
 
 namespace {
 
-// One warp per block of `rows` query rows of one sequence. x, y: the least lo and the largest hi of the rows
-// that see any key (y = 0: none does); z, w: the largest lo and the least hi of all of them, so that keys
-// z <= j < w are in every row's range (a row without a key makes that empty). Resets the ticket counter of the kernel
-// that follows, where it has one.
-__global__ void __launch_bounds__(256) row_hull_kernel(const int2* range, int4* hull, int B, int S_q, int rows,
-                                                       int n_blocks, int* ticket) {
-  if (ticket && blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
-  const long long wid = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+constexpr int kStartThreads = 256;
+
+// The small work in front of a kernel with modified scores, in one launch (three took 10 us of a training step over
+// short documents): the first blocks take a query row a thread, the others a hull a warp.
+__global__ void __launch_bounds__(kStartThreads) row_start_kernel(const __grid_constant__ RowStart a, int row_blocks) {
+  if (blockIdx.x == 0 && (int)threadIdx.x < a.n_tickets) a.tickets[threadIdx.x] = 0;
+  if ((int)blockIdx.x < row_blocks) {
+    const long long row = (long long)blockIdx.x * kStartThreads + threadIdx.x;
+    if (row >= a.n_rows) return;
+    const float l = a.lse[row];
+    a.lse2[row] = l == -INFINITY || l != l ? INFINITY : l * 1.4426950408889634f;
+    a.d[0][row] = a.d[1][row] = 0.f;
+    return;
+  }
+  long long wid = ((long long)(blockIdx.x - row_blocks) * kStartThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (wid >= (long long)B * n_blocks) return;
+  const long long first = (long long)a.B * a.blocks[0];
+  const int which = wid >= first;
+  if (which) wid -= first;
+  const int n_blocks = a.blocks[which];
+  if (wid >= (long long)a.B * n_blocks) return;
   const int b = (int)(wid / n_blocks), blk = (int)(wid - (long long)b * n_blocks);
-  const int i0 = blk * rows, i1 = min(S_q, i0 + rows);
+  const int i0 = blk * a.rows[which], i1 = min(a.S_q, i0 + a.rows[which]);
   int4 h = make_int4(0x7fffffff, 0, 0, 0x7fffffff);
   for (int i = i0 + lane; i < i1; i += 32) {
-    const int2 r = range[(long long)b * S_q + i];
+    const int2 r = a.range[(long long)b * a.S_q + i];
     const int lo = max(r.x, 0);
     if (lo < r.y) {
       h.x = min(h.x, lo);
@@ -48,17 +61,16 @@ __global__ void __launch_bounds__(256) row_hull_kernel(const int2* range, int4* 
   h.y = __reduce_max_sync(0xffffffffu, h.y);
   h.z = __reduce_max_sync(0xffffffffu, h.z);
   h.w = __reduce_min_sync(0xffffffffu, h.w);
-  if (lane == 0) hull[wid] = h;
+  if (lane == 0) a.hull[which][wid] = h;
 }
 
 }  // namespace
 
-cudaError_t launch_row_hull(const int32_t* range, void* hull, int B, int S_q, int rows, int n_blocks,
-                            int* ticket, cudaStream_t s) {
-  const long long warps = (long long)B * n_blocks;
-  row_hull_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(reinterpret_cast<const int2*>(range),
-                                                              reinterpret_cast<int4*>(hull), B, S_q, rows, n_blocks,
-                                                              ticket);
+cudaError_t launch_row_start(const RowStart& a, cudaStream_t s) {
+  const long long row_blocks = (a.n_rows + kStartThreads - 1) / kStartThreads;
+  const long long warps = (long long)a.B * (a.blocks[0] + a.blocks[1]);
+  const long long grid = row_blocks + (warps * 32 + kStartThreads - 1) / kStartThreads;
+  row_start_kernel<<<(unsigned)(grid > 0 ? grid : 1), kStartThreads, 0, s>>>(a, (int)row_blocks);
   return cudaGetLastError();
 }
 
