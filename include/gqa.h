@@ -323,7 +323,8 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  *              bf16 prefill and backward work through the blocks between a tile's least and largest key.
  * mod NULL, or nothing set in it: the plain call, bit for bit.
  * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
- * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. gqa_prefill_backward_mod needs
+ * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. Calls that share a workspace must
+ * not overlap on the GPU. gqa_prefill_backward_mod needs
  * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in
  * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take
  * gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite.

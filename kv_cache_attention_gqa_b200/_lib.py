@@ -305,6 +305,19 @@ def decode_workspace_size(B: int, h_q: int, h_kv: int, T_max: int, d_h: int, dty
     return n
 
 
+def _decode_workspace(ws, need: int, device, mod):
+    """A decode's workspace and its size: the caller's, or the stream's cached one. A captured call with modified
+    scores takes zeros from the capture's own pool, so that graphs captured on one stream can run at once and a
+    cached workspace that grows later takes nothing from them."""
+    if ws is not None:
+        return ws, _ws_bytes(ws)
+    if mod is not None and torch.cuda.is_current_stream_capturing():
+        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+    else:
+        ws = workspace(need, device)
+    return ws, ws.numel()
+
+
 _ws_lock = threading.Lock()
 _ws_cache: dict = {}
 _ws_sizes: dict = {}
@@ -314,7 +327,8 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     """A zero-filled, 256-byte aligned device workspace of at least ``nbytes``, cached per device
     and stream (every completed decode leaves its counter region at zero again)."""
     dev = torch.device(device)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    key = (index, torch._C._cuda_getCurrentRawStream(index))
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
@@ -347,17 +361,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, kv_
     need = _ws_sizes.get(key)
     if need is None:
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
-    if ws is None:
-        ws = workspace(need, q.device)
     mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    ws, nws = _decode_workspace(ws, need, q.device, mod)
     if mod is not None:
         _check("gqa_decode_mod", _lib.gqa_decode_mod(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), mod, B, h_q, h_kv, T_max,
-            d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
+            d_h, scale, int(window), dt, _ptr(ws), nws, num_splits, _stream()))
         return (out, lse) if return_lse else out
     _check("gqa_decode", _lib.gqa_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse),
                                          _ptr(kl), _ptr(qp), B, h_q, h_kv, T_max, d_h, scale,
-                                         int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
+                                         int(window), dt, _ptr(ws), nws, num_splits, _stream()))
     return (out, lse) if return_lse else out
 
 
@@ -429,19 +442,17 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     need = _ws_sizes.get(key)
     if need is None:
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
-    if ws is None:
-        ws = workspace(need, q.device)
     mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    ws, nws = _decode_workspace(ws, need, q.device, mod)
     if mod is not None:
         _check("gqa_decode_paged_mod", _lib.gqa_decode_paged_mod(
             _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), _ptr(bt), mod, B, h_q,
-            h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws), num_splits,
-            _stream()))
+            h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), nws, num_splits, _stream()))
         return (out, lse) if return_lse else out
     _check("gqa_decode_paged", _lib.gqa_decode_paged(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), _ptr(bt),
-        B, h_q, h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), _ws_bytes(ws),
-        num_splits, _stream()))
+        B, h_q, h_kv, num_pages, page_size, max_pages, d_h, scale, int(window), dt, _ptr(ws), nws, num_splits,
+        _stream()))
     return (out, lse) if return_lse else out
 
 
@@ -748,7 +759,8 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, *, q_s
     """Attention weight of every cached key, fp32 (B, h_kv, T_max): the sum over the group's heads and the
     query rows that see it of exp(scale q.k - lse). q (B, h_q, S_q, d_h) with lse (B, h_q, S_q) as returned
     by ``prefill``, or (B, h_q, d_h) with (B, h_q) by ``decode``. ``q_start`` None: the queries are the
-    last S_q cached rows. ``weights`` given: the sums are added to its entries j < kv_len, in place."""
+    last S_q cached rows. ``weights`` given: the sums are added to its entries j < kv_len, in place. The scores
+    are plain ones, so ``lse`` is one of a call without softcap, alibi_slopes and key_range."""
     if k_cache.dim() != 4 or k_cache.shape[0] != q.shape[0]:
         raise ValueError("k_cache must be (B, h_kv, T_max, d_h)")
     _, h_kv, T_max, d = k_cache.shape

@@ -299,3 +299,35 @@ def test_expired_wait_with_drawn_items():
         o, lse = gqa.prefill(q, k, v, return_lse=True, key_range=rg)
         assert torch.equal(o, want) and torch.equal(lse, want_lse)
     assert gqa.get_device_error() == 0
+
+
+def test_two_captured_decodes_at_once():
+    """Two graphs captured on one stream, replayed together on two: neither uses the other's partial results, also after
+    the stream's own workspace has grown."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, T, d = 4, 8, 2, 4000, 128
+    slopes = torch.linspace(0.01, 0.2, h_q, device="cuda")
+    calls = []
+    side = torch.cuda.Stream()
+    for seed in (1, 10):
+        q = _randn((B, h_q, d), torch.bfloat16, seed).cuda()
+        k, v = (_randn((B, h_kv, T, d), torch.bfloat16, seed + i).cuda() for i in (1, 2))
+        how = dict(softcap=20.0, alibi_slopes=slopes, return_lse=True)
+        want = gqa.decode(q, k, v, **how)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = gqa.decode(q, k, v, **how)
+        calls.append((graph, got, want, (q, k, v)))
+    with torch.cuda.stream(side):
+        gqa.workspace(1 << 26, "cuda").fill_(0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for s, (graph, *_) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _ in calls:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert gqa.get_device_error() == 0
