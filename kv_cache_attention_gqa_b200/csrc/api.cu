@@ -505,7 +505,7 @@ gqa_status gqa_prefill_mod(const void* q, const void* k_cache, const void* v_cac
   a.err = device_error_ptr();
   if (!a.err) return GQA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == GQA_FP32) return from_cuda(a.mod.on() ? launch_prefill_fp32_mod(a, s) : launch_prefill_fp32(a, s));
+  if (dtype == GQA_FP32) return from_cuda(a.mod.on() ? launch_prefill_fp32_mod(a, sm_count(), s) : launch_prefill_fp32(a, s));
   // TMA views: Q as (d_h, S_q, B*h_q) with box (64, P, H): one box holds the H heads x P
   // positions of a tile, head-major; K, V as rows (B*h_kv*T_max, d_h) with box (64, 128).
   const int H = prefill_heads_per_tile(h_q, h_kv);

@@ -154,7 +154,7 @@ struct PrefillArgs {
 };
 // fp32 check mode (scalar FFMA)
 cudaError_t launch_prefill_fp32(const PrefillArgs& a, cudaStream_t s);
-cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, cudaStream_t s);  // modified scores
+cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, int num_sms, cudaStream_t s);  // modified scores
 // bf16 tcgen05 path (sm_100a). tmaps: [0] = Q as a 3-D view (d_h, S_q, B*h_q) with box
 // (64, 128 / H, H); [1] = K, [2] = V as 2-D views (d_h, B*h_kv*T_max) with box (64, 128).
 cudaError_t launch_prefill_bf16(const PrefillArgs& a, const CUtensorMap* tmaps, int num_sms,

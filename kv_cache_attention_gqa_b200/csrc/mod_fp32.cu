@@ -4,12 +4,14 @@
 // recomputes P from the saved lse and multiplies dS by the cap's derivative 1 - tanh^2.
 //
 // 256 threads, 8 to a row of the stationary tile (16 rows x 16 threads for dkdv). A thread forms four scores from
-// 16-byte loads of both operands' rows (16 FFMA per 5 loads) and owns NC float4 columns of its row's output, where NC = ceil(d / 32):
-// the rows are padded with zeros to 32 NC columns and 4 more, which keeps 16-byte alignment and spreads the
-// banks. Key (query) tiles that no pair of the stationary tile sees are skipped. Bound: shared-memory loads, and
-// latency for the few blocks of small calls. Measured (B200), 2 x 6 heads of 67 rows over 2 KV heads,
-// d = 96: forward 29 us, dq 32 us, dk and dv 36 us; one warp per row with a shuffle reduction per key, the layout of
-// the plain check-mode kernels, took 77, 95 and 166 us.
+// 16-byte loads of both operands' rows (16 FFMA per 5 loads) and owns NC float4 columns of its row's output, where
+// NC = ceil(d / 32): the rows are padded with zeros to 32 NC columns and 4 more, which keeps 16-byte alignment and
+// spreads the banks. Key (query) tiles that no pair of the stationary tile sees are skipped. Bound: shared-memory
+// loads. Calls whose 32-row tiles leave SMs without a block are bound by latency (two warps a scheduler waiting for
+// shared memory): they take tiles of 8 rows, and of 8 keys, with a warp to each. dq and dkdv need nothing of each
+// other and are blocks of one launch. Measured (B200), 2 x 6 heads of 67 rows over 2 KV heads, d = 96: forward 18 us,
+// backward 34 us (29, and 32 + 36 in two launches, with tiles of 32 rows and 16 keys); one warp per row with a shuffle
+// reduction per key, the layout of the plain check-mode kernels, took 77 and 95 + 166 us.
 
 #include <cooperative_groups.h>
 #include <math.h>
@@ -25,8 +27,8 @@ namespace mf {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
-constexpr int kRows = 32;  // rows of a query tile; keys of a key tile (prefill, dq)
-constexpr int kKeys = 16;  // stationary keys of a dkdv block
+constexpr int kRows = 32;  // rows of a query tile (8: small calls); keys of the key tiles it meets
+constexpr int kKeys = 16;  // stationary keys of a dkdv block (8: small calls)
 constexpr int kKvQ = 64;   // query rows of its tiles
 
 struct FArgs {
@@ -88,27 +90,42 @@ __device__ __forceinline__ void load_rows(float* to, const float* from, int r0, 
   }
 }
 
-// products of one row (x) with rows y0, y0 + step, ...: four at a time
-template <int NC, int kStep>
-__device__ __forceinline__ void dot4(const float* x, const float* y, float (&s)[4]) {
-  constexpr int kStride = 32 * NC + 4;
-  s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll 4
+// products of one row (x) with the N rows y, y + kStep rows, ...; four sums are under way whatever N is
+template <int NC, int kStep, int N>
+__device__ __forceinline__ void dots(const float* x, const float* y, float (&s)[N]) {
+  constexpr int kStride = 32 * NC + 4, kSplit = 4 / N;
+  static_assert(N * kSplit == 4, "1, 2 or 4 rows");
+  float p[N][kSplit];
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+#pragma unroll
+    for (int e = 0; e < kSplit; ++e) p[u][e] = 0.f;
+#pragma unroll (N == 4 ? 4 : 8)
   for (int c = 0; c < 32 * NC; c += 4) {
     const float4 a = *reinterpret_cast<const float4*>(x + c);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < N; ++u) {
       const float4 b = *reinterpret_cast<const float4*>(y + u * kStep * kStride + c);
-      s[u] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[u]))));
+      p[u][0 % kSplit] = fmaf(a.x, b.x, p[u][0 % kSplit]);
+      p[u][1 % kSplit] = fmaf(a.y, b.y, p[u][1 % kSplit]);
+      p[u][2 % kSplit] = fmaf(a.z, b.z, p[u][2 % kSplit]);
+      p[u][3 % kSplit] = fmaf(a.w, b.w, p[u][3 % kSplit]);
     }
+  }
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    s[u] = p[u][0];
+#pragma unroll
+    for (int e = 1; e < kSplit; ++e) s[u] += p[u][e];
   }
 }
 
-// acc += w * row, over this thread's float4 columns (lane + 8 n, or kLanes in general)
+// acc += w * row, over this thread's float4 columns tx, tx + kLanes, ... of 8 NC
 template <int NC, int kLanes>
 __device__ __forceinline__ void axpy(float4* acc, float w, const float* row, int tx) {
 #pragma unroll
-  for (int n = 0; n < 8 * NC / kLanes; ++n) {
+  for (int n = 0; n < (8 * NC + kLanes - 1) / kLanes; ++n) {
+    if (8 * NC % kLanes != 0 && tx + kLanes * n >= 8 * NC) continue;
     const float4 x = *reinterpret_cast<const float4*>(row + 4 * (tx + kLanes * n));
     acc[n].x = fmaf(w, x.x, acc[n].x);
     acc[n].y = fmaf(w, x.y, acc[n].y);
@@ -120,7 +137,7 @@ __device__ __forceinline__ void axpy(float4* acc, float w, const float* row, int
 template <int NC, int kLanes>
 __device__ __forceinline__ void store_row(float* to, const float4* acc, float f, int tx, int D) {
 #pragma unroll
-  for (int n = 0; n < 8 * NC / kLanes; ++n) {
+  for (int n = 0; n < (8 * NC + kLanes - 1) / kLanes; ++n) {
     const int c = 4 * (tx + kLanes * n);
     const float x[4] = {acc[n].x, acc[n].y, acc[n].z, acc[n].w};
 #pragma unroll
@@ -129,22 +146,24 @@ __device__ __forceinline__ void store_row(float* to, const float4* acc, float f,
   }
 }
 
-// Query tiles: 32 rows of one head. kGrad: the dq pass (lse, drow and dO given), else the forward.
-template <int NC, bool kGrad>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ FArgs a) {
+// Query tiles: kR rows of one head. kGrad: the dq pass (lse, drow and dO given), else the forward.
+template <int NC, bool kGrad, int kR>
+__device__ __forceinline__ void rows_block(const FArgs& a, int block) {
   constexpr int kStride = 32 * NC + 4;
+  constexpr int kLanes = kThreads / kR, kS = kRows / kLanes;  // threads of a row, scores of a thread
+  constexpr int kN = (8 * NC + kLanes - 1) / kLanes;          // float4 columns of a thread
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);
-  float* sk = sq + kRows * kStride;
+  float* sk = sq + kR * kStride;
   float* sv = sk + kRows * kStride;
-  float* sdo = sv + kRows * kStride;               // kGrad
-  float* sp = sdo + (kGrad ? kRows * kStride : 0);  // weights of the tile: [row][key]
+  float* sdo = sv + kRows * kStride;             // kGrad
+  float* sp = sdo + (kGrad ? kR * kStride : 0);  // weights of the tile: [row][key]
   __shared__ int s_lo, s_hi;
-  const int n_tiles = (a.S_q + kRows - 1) / kRows;
-  const int tile = n_tiles - 1 - blockIdx.x % n_tiles, bh = blockIdx.x / n_tiles;  // late rows first
+  const int n_tiles = (a.S_q + kR - 1) / kR;
+  const int tile = n_tiles - 1 - block % n_tiles, bh = block / n_tiles;  // late rows first
   const int b = bh / a.h_q, head = bh - b * a.h_q, g = head / a.r;
-  const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
-  const int i = tile * kRows + ty;
+  const int ty = threadIdx.x / kLanes, tx = threadIdx.x % kLanes;
+  const int i = tile * kR + ty;
   const int kv = a.kv_len ? a.kv_len[b] : a.T_max;
   const int qs = a.q_start ? a.q_start[b] : 0;
   const bool valid = kv >= 1 && kv <= a.T_max && qs >= 0;
@@ -170,53 +189,55 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     atomicMax(&s_hi, see.y);
   }
   const float* qp = a.q + (long long)bh * a.S_q * a.D;
-  load_rows<NC, kRows>(sq, qp, tile * kRows, 0, a.S_q, a.D);
-  if (kGrad) load_rows<NC, kRows>(sdo, a.d_o + (long long)bh * a.S_q * a.D, tile * kRows, 0, a.S_q, a.D);
+  load_rows<NC, kR>(sq, qp, tile * kR, 0, a.S_q, a.D);
+  if (kGrad) load_rows<NC, kR>(sdo, a.d_o + (long long)bh * a.S_q * a.D, tile * kR, 0, a.S_q, a.D);
   __syncthreads();
   const int lo = s_lo, hi = s_hi;
   const float slope = a.slopes ? a.slopes[head] : 0.f;
   const long long kvb = ((long long)b * a.h_kv + g) * a.T_max * a.D;
-  float4 acc[NC];
+  float4 acc[kN];
 #pragma unroll
-  for (int n = 0; n < NC; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int n = 0; n < kN; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
   for (int k0 = lo / kRows * kRows; k0 < hi; k0 += kRows) {
     if (!__syncthreads_or(see.x < k0 + kRows && see.y > k0)) continue;  // (also: the last tile's readers are done)
     load_rows<NC, kRows>(sk, a.k + kvb, k0, lo, hi, a.D);
     load_rows<NC, kRows>(sv, a.v + kvb, k0, lo, hi, a.D);
     __syncthreads();
-    float s[4], t[4], w[4];
-    dot4<NC, 8>(sq + ty * kStride, sk + tx * kStride, s);
+    float s[kS], t[kS], w[kS];
+    dots<NC, kLanes, kS>(sq + ty * kStride, sk + tx * kStride, s);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int key = k0 + tx + 8 * u;
+    for (int u = 0; u < kS; ++u) {
+      const int key = k0 + tx + kLanes * u;
       s[u] = mod_score(s[u], a.scale, a.cap, slope, pos - key, &t[u]);
       if (key < see.x || key >= see.y) s[u] = -INFINITY;
     }
     if constexpr (kGrad) {
-      float dp[4];
-      dot4<NC, 8>(sdo + ty * kStride, sv + tx * kStride, dp);
+      float dp[kS];
+      dots<NC, kLanes, kS>(sdo + ty * kStride, sv + tx * kStride, dp);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kS; ++u)
         w[u] = s[u] == -INFINITY ? 0.f : expf(s[u] - lse) * (dp[u] - dr) * (1.f - t[u] * t[u]);
     } else {
-      float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+      float mx = s[0];
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      for (int u = 1; u < kS; ++u) mx = fmaxf(mx, s[u]);
+#pragma unroll
+      for (int off = 1; off < kLanes; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float mn = fmaxf(m, mx);
       const float f = m == -INFINITY ? 0.f : expf(m - mn);
       float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kS; ++u) {
         w[u] = s[u] == -INFINITY ? 0.f : expf(s[u] - mn);
         sum += w[u];
       }
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       l = fmaf(l, f, sum);
       m = mn;
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
+      for (int n = 0; n < kN; ++n) {
         acc[n].x *= f;
         acc[n].y *= f;
         acc[n].z *= f;
@@ -224,52 +245,58 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) sp[ty * kRows + tx + 8 * u] = w[u];
-    __syncwarp();  // a row's eight threads share a warp
+    for (int u = 0; u < kS; ++u) sp[ty * kRows + tx + kLanes * u] = w[u];
+    __syncwarp();  // a row's threads share a warp
     const float* from = kGrad ? sk : sv;
 #pragma unroll 4
-    for (int j = 0; j < kRows; ++j) axpy<NC, 8>(acc, sp[ty * kRows + j], from + j * kStride, tx);
+    for (int j = 0; j < kRows; ++j) axpy<NC, kLanes>(acc, sp[ty * kRows + j], from + j * kStride, tx);
   }
   if (i >= a.S_q) return;
   if (!kGrad) {
     if (valid && l == 0.f && tx == 0 && !a.range) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
     if (a.lse && tx == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
   }
-  store_row<NC, 8>(a.out + row * a.D, acc, kGrad ? a.scale : l > 0.f ? 1.f / l : 0.f, tx, a.D);
+  store_row<NC, kLanes>(a.out + row * a.D, acc, kGrad ? a.scale : l > 0.f ? 1.f / l : 0.f, tx, a.D);
 }
 
-// Key tiles: 16 keys of one (sequence, KV head), all rows of all its heads that see them. The (head, 64 rows) tiles are
+template <int NC, int kR>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ FArgs a) {
+  rows_block<NC, false, kR>(a, blockIdx.x);
+}
+
+// Key tiles: kK keys of one (sequence, KV head), all rows of all its heads that see them. The (head, 64 rows) tiles are
 // shared by the blocks of a cluster, whose sums meet through distributed shared memory in the order of their ranks.
-template <int NC>
-__global__ void __launch_bounds__(kThreads) keys_kernel(const __grid_constant__ FArgs a) {
+template <int NC, int kK>
+__device__ __forceinline__ void keys_block(const FArgs& a) {
   constexpr int kStride = 32 * NC + 4;
+  constexpr int kLanes = kThreads / kK, kS = kKvQ / kLanes;  // threads of a key, scores of a thread
   extern __shared__ float4 smem4[];
   float* sk = reinterpret_cast<float*>(smem4);
-  float* sv = sk + kKeys * kStride;
-  float* sq = sv + kKeys * kStride;
+  float* sv = sk + kK * kStride;
+  float* sq = sv + kK * kStride;
   float* sdo = sq + kKvQ * kStride;
   float* sp = sdo + kKvQ * kStride;  // [key][row]: P, then dS
-  float* sds = sp + kKeys * kKvQ;
+  float* sds = sp + kK * kKvQ;
   __shared__ int2 s_see[kKvQ];
   __shared__ float s_lse[kKvQ], s_dr[kKvQ];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int n_tiles = (a.T_max + kKeys - 1) / kKeys;
+  const int n_tiles = (a.T_max + kK - 1) / kK;
   const int tile = blockIdx.x / ranks % n_tiles, bg = blockIdx.x / ranks / n_tiles;
   const int b = bg / a.h_kv, g = bg - b * a.h_kv;
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int k0 = tile * kKeys, key = k0 + ty;
+  const int ty = threadIdx.x / kLanes, tx = threadIdx.x % kLanes;
+  const int k0 = tile * kK, key = k0 + ty;
   const int kv = a.kv_len ? a.kv_len[b] : a.T_max;
   const int qs = a.q_start ? a.q_start[b] : 0;
   const bool valid = kv >= 1 && kv <= a.T_max && qs >= 0;
-  constexpr int kN = (8 * NC + 15) / 16;  // float4 columns of a thread
+  constexpr int kN = (8 * NC + kLanes - 1) / kLanes;  // float4 columns of a thread
   float4 ak[kN], av[kN];
 #pragma unroll
   for (int n = 0; n < kN; ++n) ak[n] = av[n] = make_float4(0.f, 0.f, 0.f, 0.f);
   const long long kvb = (long long)bg * a.T_max * a.D;
   if (valid && k0 < kv) {
-    load_rows<NC, kKeys>(sk, a.k + kvb, k0, 0, kv, a.D);
-    load_rows<NC, kKeys>(sv, a.v + kvb, k0, 0, kv, a.D);
+    load_rows<NC, kK>(sk, a.k + kvb, k0, 0, kv, a.D);
+    load_rows<NC, kK>(sv, a.v + kvb, k0, 0, kv, a.D);
     const int nq = (a.S_q + kKvQ - 1) / kKvQ;
     for (long long it = rank; it < (long long)a.r * nq; it += ranks) {
       const int head = g * a.r + (int)(it / nq), i0 = (int)(it % nq) * kKvQ;
@@ -282,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) keys_kernel(const __grid_constant__ 
         int2 see = i < a.S_q ? row_keys(a, b, i, (long long)qs + i, kv) : make_int2(0, 0);
         const float l = i < a.S_q ? a.lse_in[base + i] : -INFINITY;
         if (!(l > -INFINITY)) see = make_int2(0, 0);
-        any = see.x < k0 + kKeys && see.y > k0;
+        any = see.x < k0 + kK && see.y > k0;
         s_see[threadIdx.x] = see;
         s_lse[threadIdx.x] = l;
         s_dr[threadIdx.x] = i < a.S_q ? a.drow[base + i] : 0.f;
@@ -291,12 +318,12 @@ __global__ void __launch_bounds__(kThreads) keys_kernel(const __grid_constant__ 
       load_rows<NC, kKvQ>(sq, a.q + base * a.D, i0, 0, a.S_q, a.D);
       load_rows<NC, kKvQ>(sdo, a.d_o + base * a.D, i0, 0, a.S_q, a.D);
       __syncthreads();
-      float s[4], dp[4];
-      dot4<NC, 16>(sk + ty * kStride, sq + tx * kStride, s);
-      dot4<NC, 16>(sv + ty * kStride, sdo + tx * kStride, dp);
+      float s[kS], dp[kS];
+      dots<NC, kLanes, kS>(sk + ty * kStride, sq + tx * kStride, s);
+      dots<NC, kLanes, kS>(sv + ty * kStride, sdo + tx * kStride, dp);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int x = tx + 16 * u;
+      for (int u = 0; u < kS; ++u) {
+        const int x = tx + kLanes * u;
         const int2 see = s_see[x];
         float t;
         const float z = mod_score(s[u], a.scale, a.cap, slope, (long long)qs + i0 + x - key, &t);
@@ -304,14 +331,14 @@ __global__ void __launch_bounds__(kThreads) keys_kernel(const __grid_constant__ 
         sp[ty * kKvQ + x] = p;
         sds[ty * kKvQ + x] = p == 0.f ? 0.f : p * (dp[u] - s_dr[x]) * (1.f - t * t);
       }
-      __syncwarp();  // a key's sixteen threads share a warp
+      __syncwarp();  // a key's threads share a warp
 #pragma unroll 4
       for (int x = 0; x < kKvQ; ++x) {
         const float p = sp[ty * kKvQ + x], ds = sds[ty * kKvQ + x];
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          const int c = 4 * (tx + 16 * n);
-          if (kN * 16 > 8 * NC && c >= 32 * NC) continue;
+          const int c = 4 * (tx + kLanes * n);
+          if (kN * kLanes > 8 * NC && c >= 32 * NC) continue;
           const float4 d = *reinterpret_cast<const float4*>(sdo + x * kStride + c);
           const float4 q = *reinterpret_cast<const float4*>(sq + x * kStride + c);
           av[n].x = fmaf(p, d.x, av[n].x);
@@ -332,20 +359,31 @@ __global__ void __launch_bounds__(kThreads) keys_kernel(const __grid_constant__ 
   constexpr int kW = 32 * NC;
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
-    const int c = 4 * (tx + 16 * n);
-    if (kN * 16 > 8 * NC && c >= kW) continue;
+    const int c = 4 * (tx + kLanes * n);
+    if (kN * kLanes > 8 * NC && c >= kW) continue;
     *reinterpret_cast<float4*>(part + ty * kW + c) = ak[n];
-    *reinterpret_cast<float4*>(part + (kKeys + ty) * kW + c) = av[n];
+    *reinterpret_cast<float4*>(part + (kK + ty) * kW + c) = av[n];
   }
   cluster.sync();
-  for (int e = rank * kThreads + threadIdx.x; e < 2 * kKeys * kW; e += ranks * kThreads) {
-    const int y = e / kW, c = e - y * kW, is_v = y / kKeys, j = k0 + y - is_v * kKeys;
+  for (int e = rank * kThreads + threadIdx.x; e < 2 * kK * kW; e += ranks * kThreads) {
+    const int y = e / kW, c = e - y * kW, is_v = y / kK, j = k0 + y - is_v * kK;
     if (c >= a.D || j >= a.T_max) continue;
     float sum = 0.f;
     for (int k = 0; k < ranks; ++k) sum += cluster.map_shared_rank(part, k)[e];
     (is_v ? a.dv : a.dk)[kvb + (long long)j * a.D + c] = valid && j < kv ? (is_v ? sum : sum * a.scale) : 0.f;
   }
   cluster.sync();  // no block leaves while its sums may be read
+}
+
+// The first key_blocks blocks (whole clusters) take key tiles, the others query tiles.
+template <int NC, int kR, int kK>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ FArgs a, int key_blocks,
+                                                            int row_blocks) {
+  if ((int)blockIdx.x < key_blocks) {
+    keys_block<NC, kK>(a);
+  } else if ((int)blockIdx.x - key_blocks < row_blocks) {
+    rows_block<NC, true, kR>(a, blockIdx.x - key_blocks);
+  }
 }
 
 // D = rowsum(dO * O), one warp per row
@@ -360,8 +398,8 @@ __global__ void __launch_bounds__(kThreads) rowsum_kernel(const __grid_constant_
   if (lane == 0) drow[row] = s;
 }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kern, long long blocks, size_t smem, const FArgs& f, cudaStream_t s, int ranks = 1) {
+template <typename Kernel, typename... Args>
+cudaError_t launch(Kernel kern, long long blocks, size_t smem, cudaStream_t s, int ranks, const Args&... args) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // the opt-in is set on every call: a check-mode call is no hot path
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -377,26 +415,30 @@ cudaError_t launch(Kernel kern, long long blocks, size_t smem, const FArgs& f, c
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, f);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NC>
+// query tiles of `rows` rows
+long long row_tiles(const FArgs& f, int rows) { return (long long)f.B * f.h_q * ((f.S_q + rows - 1) / rows); }
+
+template <int NC, int kR>
 cudaError_t forward(const FArgs& f, cudaStream_t s) {
-  const size_t smem = (3 * kRows * (32 * NC + 4) + kRows * kRows) * sizeof(float);
-  return launch(rows_kernel<NC, false>, (long long)f.B * f.h_q * ((f.S_q + kRows - 1) / kRows), smem, f, s);
+  const size_t smem = ((kR + 2 * kRows) * (32 * NC + 4) + kR * kRows) * sizeof(float);
+  return launch(rows_kernel<NC, kR>, row_tiles(f, kR), smem, s, 1, f);
 }
-template <int NC>
+template <int NC, int kR, int kK>
 cudaError_t backward(const FArgs& f, int num_sms, cudaStream_t s) {
-  size_t smem = (4 * kRows * (32 * NC + 4) + kRows * kRows) * sizeof(float);
-  cudaError_t e = launch(rows_kernel<NC, true>, (long long)f.B * f.h_q * ((f.S_q + kRows - 1) / kRows), smem, f, s);
-  if (e != cudaSuccess) return e;
-  smem = (2 * (kKeys + kKvQ) * (32 * NC + 4) + 2 * kKeys * kKvQ) * sizeof(float);
+  const size_t row_smem = ((2 * kR + 2 * kRows) * (32 * NC + 4) + kR * kRows) * sizeof(float);
+  const size_t key_smem = (2 * (kK + kKvQ) * (32 * NC + 4) + 2 * kK * kKvQ) * sizeof(float);
   // blocks of a cluster: up to 8, while there are tiles for them and SMs without a block
-  const long long tiles = (long long)f.B * f.h_kv * ((f.T_max + kKeys - 1) / kKeys);
+  const long long tiles = (long long)f.B * f.h_kv * ((f.T_max + kK - 1) / kK);
   const long long its = (long long)f.r * ((f.S_q + kKvQ - 1) / kKvQ);
   int ranks = 1;
   while (ranks < 8 && 2 * ranks <= its && 2 * ranks * tiles <= 2 * num_sms) ranks *= 2;
-  return launch(keys_kernel<NC>, tiles * ranks, smem, f, s, ranks);
+  const long long keys = tiles * ranks, rows = row_tiles(f, kR), blocks = keys + (rows + ranks - 1) / ranks * ranks;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch(backward_kernel<NC, kR, kK>, blocks, row_smem > key_smem ? row_smem : key_smem, s, ranks, f,
+                (int)keys, (int)rows);
 }
 
 template <typename F>
@@ -414,7 +456,7 @@ cudaError_t by_width(int D, F&& f) {
 
 }  // namespace mf
 
-cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, cudaStream_t s) {
+cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, int num_sms, cudaStream_t s) {
   mf::FArgs f = {};
   f.q = reinterpret_cast<const float*>(a.q);
   f.k = reinterpret_cast<const float*>(a.k);
@@ -437,7 +479,10 @@ cudaError_t launch_prefill_fp32_mod(const PrefillArgs& a, cudaStream_t s) {
   f.slopes = a.mod.slopes;
   f.range = reinterpret_cast<const int2*>(a.mod.range);
   f.err = a.err;
-  return mf::by_width(a.d_h, [&](auto nc) { return mf::forward<decltype(nc)::value>(f, s); });
+  const bool small = mf::row_tiles(f, mf::kRows) < num_sms;
+  return mf::by_width(a.d_h, [&](auto nc) {
+    return small ? mf::forward<decltype(nc)::value, 8>(f, s) : mf::forward<decltype(nc)::value, mf::kRows>(f, s);
+  });
 }
 
 cudaError_t launch_backward_fp32_mod(const BackwardArgs& a, int num_sms, cudaStream_t s) {
@@ -473,7 +518,11 @@ cudaError_t launch_backward_fp32_mod(const BackwardArgs& a, int num_sms, cudaStr
   mf::rowsum_kernel<<<(unsigned)((rows * 32 + mf::kThreads - 1) / mf::kThreads), mf::kThreads, 0, s>>>(f, a.drow);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return mf::by_width(a.d_h, [&](auto nc) { return mf::backward<decltype(nc)::value>(f, num_sms, s); });
+  const bool small = mf::row_tiles(f, mf::kRows) < num_sms;
+  return mf::by_width(a.d_h, [&](auto nc) {
+    return small ? mf::backward<decltype(nc)::value, 8, 8>(f, num_sms, s)
+                 : mf::backward<decltype(nc)::value, mf::kRows, mf::kKeys>(f, num_sms, s);
+  });
 }
 
 }  // namespace gqa

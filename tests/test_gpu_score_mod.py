@@ -331,3 +331,27 @@ def test_two_captured_decodes_at_once():
     for _, got, want, _ in calls:
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [24, 96, 200])
+def test_check_mode_with_many_tiles(d):
+    """More 32-row tiles than SMs: the check mode's large tiles (smaller calls take tiles of 8)."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S = 2, 12, 4, 213
+    slopes = torch.linspace(0.0, 0.3, h_q)
+    rg = torch.tensor([[lo, hi] for lo, hi in ((0, 90), (90, 90), (60, 140), (140, S)) for _ in range(54)],
+                      dtype=torch.int32)[None, :S].repeat(B, 1, 1).contiguous()
+    q, k, v, up = (_randn((B, h, S, d), torch.float32, i) for i, h in ((1, h_q), (2, h_kv), (3, h_kv), (4, h_q)))
+    kv = [S, 170]
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), kv_len=kv, causal=False, softcap=9.0,
+                                        slopes=slopes.numpy(), key_range=rg.numpy(), d_o=up.double())
+    k[1, :, 170:], v[1, :, 170:] = float("nan"), float("nan")
+    q, k, v, up = q.cuda(), k.cuda(), v.cuda(), up.cuda()
+    how = dict(kv_len=torch.tensor(kv, dtype=torch.int32).cuda(), causal=False, softcap=9.0, alibi_slopes=slopes.cuda(),
+               key_range=rg.cuda())
+    o, lse = gqa.prefill(q, k, v, return_lse=True, **how)
+    _check(o, lse, ref, torch.float32, "prefill")
+    for name, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, **how), ref[3:]):
+        assert_grad_close(got.double().cpu().numpy(), want, name, fp32=True)
+    assert gqa.get_device_error() == 0
