@@ -326,8 +326,9 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. Calls that share a workspace must
  * not overlap on the GPU. gqa_prefill_backward_mod needs
  * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in
- * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take
- * gqa_decode's workspace. Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite.
+ * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take a
+ * workspace as gqa_decode does, of gqa_decode_mod_workspace_size bytes (automatic chunks are smaller than
+ * gqa_decode's). Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite.
  */
 typedef struct {
   float softcap;             /* > 0: cap of the scores; 0: none */
@@ -349,6 +350,8 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
                                     int T_max, int d_h, float scale, int causal, int window,
                                     gqa_dtype dtype, void* workspace, size_t workspace_bytes,
                                     void* stream);
+size_t gqa_decode_mod_workspace_size(int B, int h_q, int h_kv, int T_max, int d_h, gqa_dtype dtype,
+                                     int num_splits);
 gqa_status gqa_decode_mod(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
                           const int32_t* kv_len, const int32_t* q_pos, const gqa_score_mod* mod, int B,
                           int h_q, int h_kv, int T_max, int d_h, float scale, int window,

@@ -75,6 +75,7 @@ SIGNATURES = {
     "gqa_prefill_backward_mod_workspace_size": (_Z, [_I, _I, _I, _I]),
     "gqa_prefill_backward_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _I,
                                       _F, _I, _I, _I, _P, _Z, _P]),
+    "gqa_decode_mod_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "gqa_decode_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _F, _I, _I, _P, _Z, _I, _P]),
     "gqa_decode_paged_mod": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _M, _I, _I, _I, _I, _I, _I, _I, _F, _I,
                                   _I, _P, _Z, _I, _P]),
@@ -189,10 +190,15 @@ def _scale(scale) -> float:
     return 0.0 if scale is None else float(scale)
 
 
+# The current device's index, without torch.cuda.current_device's check that CUDA is up: for calls that have seen a
+# CUDA tensor.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream():
     """The raw handle of the current stream (torch.cuda.current_stream() builds an object around it, which
     costs more than the launch of a small kernel)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(_device())
 
 
 def debug_expire_waits(enable: bool) -> None:
@@ -204,6 +210,7 @@ def debug_expire_waits(enable: bool) -> None:
 def get_device_error() -> int:
     """Synchronise the current stream, read and clear the sticky device error word."""
     code = ctypes.c_int(0)
+    torch.cuda.init()
     st = _lib.gqa_get_device_error(ctypes.byref(code), _stream())
     if st not in (GQA_OK, 4):
         raise GQAError("gqa_get_device_error", st)
@@ -276,8 +283,8 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, q_
     dt = _dtype_code(q)
     if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
-    out = _out(out, q.shape, q.dtype, q.device)
-    lse = torch.empty((B, h_q, S_q), dtype=torch.float32, device=q.device) if return_lse else None
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, q.dtype, q.device)
+    lse = q.new_empty((B, h_q, S_q), dtype=torch.float32) if return_lse else None
     qs = _int_vec(q_start, B, q.device, "q_start")
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     scale = _scale(scale)
@@ -297,11 +304,13 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, q_
 
 
 def decode_workspace_size(B: int, h_q: int, h_kv: int, T_max: int, d_h: int, dtype=torch.bfloat16,
-                          num_splits: int = 0) -> int:
+                          num_splits: int = 0, modified: bool = False) -> int:
+    """Bytes of workspace of a decode call (``modified``: with softcap, alibi_slopes or key_range)."""
     dt = GQA_BF16 if dtype == torch.bfloat16 else GQA_FP32
-    n = _lib.gqa_decode_workspace_size(B, h_q, h_kv, T_max, d_h, dt, num_splits)
+    name = "gqa_decode_mod_workspace_size" if modified else "gqa_decode_workspace_size"
+    n = getattr(_lib, name)(B, h_q, h_kv, T_max, d_h, dt, num_splits)
     if n == 0:
-        raise GQAError("gqa_decode_workspace_size", 1)
+        raise GQAError(name, 1)
     return n
 
 
@@ -352,16 +361,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, kv_
     dt = _dtype_code(q)
     if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
-    out = _out(out, q.shape, q.dtype, q.device)
-    lse = torch.empty((B, h_q), dtype=torch.float32, device=q.device) if return_lse else None
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, q.dtype, q.device)
+    lse = q.new_empty((B, h_q), dtype=torch.float32) if return_lse else None
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     qp = _int_vec(q_pos, B, q.device, "q_pos")
     scale = _scale(scale)
-    key = (B, h_q, h_kv, T_max, d_h, dt, num_splits, q.device.index)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    key = (B, h_q, h_kv, T_max, d_h, dt, num_splits, q.device.index, mod is None)
     need = _ws_sizes.get(key)
     if need is None:
-        need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
-    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+        need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits, mod is not None)
     ws, nws = _decode_workspace(ws, need, q.device, mod)
     if mod is not None:
         _check("gqa_decode_mod", _lib.gqa_decode_mod(
@@ -388,8 +397,8 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     dt = _dtype_code(q)
     if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
-    out = _out(out, q.shape, q.dtype, q.device)
-    lse = torch.empty((B, h_q), dtype=torch.float32, device=q.device) if return_lse else None
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, q.dtype, q.device)
+    lse = q.new_empty((B, h_q), dtype=torch.float32) if return_lse else None
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     qp = _int_vec(q_pos, B, q.device, "q_pos")
     scale = _scale(scale)
@@ -432,17 +441,17 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
         raise TypeError("q, k_pages and v_pages must share one dtype")
     bt = _block_table(block_table, B, q.device)
     max_pages = bt.shape[1]
-    out = _out(out, q.shape, q.dtype, q.device)
-    lse = torch.empty((B, h_q), dtype=torch.float32, device=q.device) if return_lse else None
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, q.dtype, q.device)
+    lse = q.new_empty((B, h_q), dtype=torch.float32) if return_lse else None
     kl = _int_vec(kv_len, B, q.device, "kv_len")
     qp = _int_vec(q_pos, B, q.device, "q_pos")
     scale = _scale(scale)
     T_max = max_pages * page_size
-    key = (B, h_q, h_kv, T_max, d_h, dt, num_splits, q.device.index)
+    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+    key = (B, h_q, h_kv, T_max, d_h, dt, num_splits, q.device.index, mod is None)
     need = _ws_sizes.get(key)
     if need is None:
-        need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits)
-    mod = _score_mod(softcap, alibi_slopes, key_range, h_q, (B, 2))
+        need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits, mod is not None)
     ws, nws = _decode_workspace(ws, need, q.device, mod)
     if mod is not None:
         _check("gqa_decode_paged_mod", _lib.gqa_decode_paged_mod(
@@ -552,7 +561,7 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, d_v: int = 512, *, kv_len=N
 
 def _on_device(*ts):
     """Every tensor given is a CUDA tensor on the current device (as _need_cuda, for strided inputs)."""
-    dev = torch.cuda.current_device()
+    dev = _device() if ts[0].is_cuda else -2
     for t in ts:
         if t is None or t.get_device() == dev:
             continue
@@ -704,8 +713,8 @@ def kv_rope_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_
     B, h_q, S, dt, inv_freq, pos_t, at, per_token, q_out = _rope_append(
         q, k_new, v_new, k_cache, v_cache, h_kv, d, pos, inv_freq, positions, offset, q_out)
     _check("kv_rope_append", _lib.kv_rope_append(
-        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(inv_freq), _ptr(pos_t),
-        _ptr(at), per_token, B, h_q, h_kv, S, T_max, d, 2 * inv_freq.numel(), offset, _strides(q),
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        inv_freq.data_ptr(), pos_t.data_ptr(), _ptr(at), per_token, B, h_q, h_kv, S, T_max, d, 2 * inv_freq.numel(), offset, _strides(q),
         _strides(k_new), _strides(v_new), 1 if interleaved else 0, scale, dt, _stream()))
     return q_out
 
@@ -720,8 +729,8 @@ def kv_rope_append_paged(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         q, k_new, v_new, k_pages, v_pages, h_kv, d, pos, inv_freq, positions, offset, q_out)
     bt = _block_table(block_table, B, q.device)
     _check("kv_rope_append_paged", _lib.kv_rope_append_paged(
-        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _ptr(inv_freq), _ptr(pos_t),
-        _ptr(at), per_token, _ptr(bt), B, h_q, h_kv, S, num_pages, page_size, bt.shape[1], d, 2 * inv_freq.numel(),
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        inv_freq.data_ptr(), pos_t.data_ptr(), _ptr(at), per_token, bt.data_ptr(), B, h_q, h_kv, S, num_pages, page_size, bt.shape[1], d, 2 * inv_freq.numel(),
         offset, _strides(q), _strides(k_new), _strides(v_new), 1 if interleaved else 0, scale, dt, _stream()))
     return q_out
 
@@ -804,12 +813,11 @@ def _evict_args(k, v, weights, B, h_kv, T_max, T_out, budget, kv_len, weights_ou
             raise ValueError("weights_out must be given when the caches are not shortened in place")
         weights_out = weights
     _out(weights_out, (B, h_kv, T_out), torch.float32, weights.device)
-    if kept is None:  # one allocation for both
-        small = torch.empty(B * (h_kv * budget + 1), dtype=torch.int32, device=weights.device)
-        kept, new_len = small[B:].view(B, h_kv, budget), small[:B]
+    if kept is None:
+        kept = weights.new_empty((B, h_kv, budget), dtype=torch.int32)
     else:
-        kept = _out(kept, (B, h_kv, budget), torch.int32, weights.device)
-        new_len = torch.empty(B, dtype=torch.int32, device=weights.device)
+        _out(kept, (B, h_kv, budget), torch.int32, weights.device)
+    new_len = weights.new_empty(B, dtype=torch.int32)
     return dt, budget, weights_out, kept, new_len, _int_vec(kv_len, B, weights.device, "kv_len")
 
 

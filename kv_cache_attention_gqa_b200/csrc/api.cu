@@ -142,7 +142,8 @@ gqa_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
     return GQA_ERR_WORKSPACE;
   const int sms = sm_count();
   if (sms <= 0) return GQA_ERR_CUDA;
-  if (workspace_bytes < decode_workspace_bytes(B, h_q, h_kv, T_max, d_h, num_splits, sms))
+  if (workspace_bytes < decode_workspace_bytes(B, h_q, h_kv, T_max, d_h, num_splits, sms, false, false,
+                                               score_mod(mod).on()))
     return GQA_ERR_WORKSPACE;
   DecodeArgs a;
   a.q = q;
@@ -631,13 +632,24 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
   return from_cuda(launch_backward_bf16(a, maps, sms, s));
 }
 
-size_t gqa_decode_workspace_size(int B, int h_q, int h_kv, int T_max, int d_h, gqa_dtype dtype,
-                                 int num_splits) {
+namespace {
+size_t decode_workspace_size(int B, int h_q, int h_kv, int T_max, int d_h, gqa_dtype dtype, int num_splits, bool mod) {
   if (B <= 0 || h_q <= 0 || h_kv <= 0 || T_max <= 0 || d_h <= 0 || h_q % h_kv != 0) return 0;
   if (num_splits < 0 || (dtype != GQA_BF16 && dtype != GQA_FP32)) return 0;
   const int sms = num_splits > 0 ? 1 : sm_count();
   if (sms <= 0) return 0;
-  return decode_workspace_bytes(B, h_q, h_kv, T_max, d_h, num_splits, sms);
+  return decode_workspace_bytes(B, h_q, h_kv, T_max, d_h, num_splits, sms, false, false, mod);
+}
+}  // namespace
+
+size_t gqa_decode_workspace_size(int B, int h_q, int h_kv, int T_max, int d_h, gqa_dtype dtype,
+                                 int num_splits) {
+  return decode_workspace_size(B, h_q, h_kv, T_max, d_h, dtype, num_splits, false);
+}
+
+size_t gqa_decode_mod_workspace_size(int B, int h_q, int h_kv, int T_max, int d_h, gqa_dtype dtype,
+                                     int num_splits) {
+  return decode_workspace_size(B, h_q, h_kv, T_max, d_h, dtype, num_splits, true);
 }
 
 gqa_status gqa_decode(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,

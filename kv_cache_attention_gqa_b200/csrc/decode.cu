@@ -54,6 +54,10 @@ constexpr int kTile = 64;           // keys per pipeline stage
 constexpr int kMaxBatch = 1024;
 constexpr int kHeadsPerUnitMax = 32;
 constexpr int kMinChunkAuto = 128;  // keys; automatic chunking never goes below this
+// With modified scores it goes down to this, or to the units' mean length where that is less: many short sequences
+// (the first tokens after a prompt of a few words) then spread over the SMs. Nine sequences of one key and 4 KV heads
+// took 113 us with 128 keys a chunk, all 36 units one after the other in one CTA.
+constexpr int kMinChunkMod = 16;
 // Automatic chunking: one chunk per SM. Each chunk boundary costs a piece epilogue (a cross-warp
 // merge and a partial write) that stalls the stream for ~2 us, which measured more than the load
 // imbalance that finer chunks would remove (decode_8k, B200: one chunk per SM was fastest for
@@ -269,7 +273,11 @@ __device__ void build_plan(const KArgs& a, Plan& p, long long* pre, int* nlen, i
   if (a.auto_chunk) {
     // at least kMinChunkAuto keys, and at least 16 keys per query row, so the partial written per
     // chunk (hpu x d_h fp32) stays small against the chunk's K/V bytes (2 x C x d_h bf16)
-    const long long lo = udiv((long long)a.min_chunk + a.gran - 1, a.gran);
+    long long lo = udiv((long long)a.min_chunk + a.gran - 1, a.gran);
+    if (a.min_chunk <= kMinChunkMod) {
+      const long long units = (long long)a.B * p.UPB, mean = udiv(p.K + units - 1, units);
+      if (lo > mean) lo = mean;
+    }
     if (C < lo) C = lo;
   }
   if (C < 1) C = 1;
@@ -1985,8 +1993,9 @@ cudaError_t launch_bf16_typed(const KArgs& ka, const CUtensorMap* tm, int grid, 
   return launch_merge<__nv_bfloat16, true>(ka, s);
 }
 
-int auto_n_max(long long K_max, int sms) {
-  long long n = (K_max + kMinChunkAuto - 1) / kMinChunkAuto;
+int auto_n_max(long long K_max, int T_max, int sms, bool mod) {
+  const int least = !mod ? kMinChunkAuto : T_max < kMinChunkMod ? T_max : kMinChunkMod;
+  long long n = (K_max + least - 1) / least;
   const long long cap = (long long)kChunksPerSm * (sms > 0 ? sms : 1);
   if (n > cap) n = cap;
   return (int)(n < 1 ? 1 : n);
@@ -2013,7 +2022,7 @@ KArgs make_kargs(const DecodeArgs& a) {
   const long long K_max = (long long)a.B * a.h_kv * ((r + hpu - 1) / hpu) * a.T_max;
   const int n_max = !auto_chunk ? a.num_splits
                     : a.mla_tc  ? auto_n_max_mla_tc(K_max, a.num_sms)
-                                : auto_n_max(K_max, a.num_sms);
+                                : auto_n_max(K_max, a.T_max, a.num_sms, a.mod.on());
   const Layout L = make_layout(a.B, a.h_q, a.h_kv, d_out, n_max, hpu_max);
   KArgs k;
   k.q = a.q;
@@ -2038,7 +2047,7 @@ KArgs make_kargs(const DecodeArgs& a) {
   // at least 16 keys per query row, so the partial written per chunk (hpu x d_out fp32) stays
   // small against the chunk's K/V bytes; the tensor-core MLA kernel is bound by its MMAs instead
   // and wants every pair of SMs busy
-  k.min_chunk = a.mla_tc ? kMlaTcMinChunk : (16 * L.hpu > kMinChunkAuto ? 16 * L.hpu : kMinChunkAuto);
+  k.min_chunk = a.mla_tc ? kMlaTcMinChunk : a.mod.on() ? kMinChunkMod : (16 * L.hpu > kMinChunkAuto ? 16 * L.hpu : kMinChunkAuto);
   // the compute-bound tensor-core MLA kernel gives up a few idle SMs for chunks that never hold
   // two pieces; the HBM-bound kernels keep every SM streaming
   k.align_units = a.mla_tc && auto_chunk ? 1 : 0;
@@ -2064,14 +2073,14 @@ KArgs make_kargs(const DecodeArgs& a) {
 }  // namespace dec
 
 size_t decode_workspace_bytes(int B, int h_q, int h_kv, int T_max, int d_h, int num_splits,
-                              int num_sms, bool mla, bool mla_tc) {
+                              int num_sms, bool mla, bool mla_tc, bool mod) {
   const int r = h_q / h_kv;
   const int hpu_max = dec::mla_heads_per_unit(mla, mla_tc);
   const int hpu = r < hpu_max ? r : hpu_max;
   const long long K_max = (long long)B * h_kv * ((r + hpu - 1) / hpu) * T_max;
   const int n_max = num_splits != 0 ? num_splits
                     : mla_tc        ? dec::auto_n_max_mla_tc(K_max, num_sms)
-                                    : dec::auto_n_max(K_max, num_sms);
+                                    : dec::auto_n_max(K_max, T_max, num_sms, mod);
   return dec::make_layout(B, h_q, h_kv, d_h, n_max, hpu_max).total;
 }
 

@@ -238,7 +238,7 @@ gqa_status decode_check_args(const void* q, const void* k_cache, const void* v_c
 
 // Workspace bytes for a decode of this shape (layout in decode.cu).
 size_t decode_workspace_bytes(int B, int h_q, int h_kv, int T_max, int d_h, int num_splits,
-                              int num_sms, bool mla = false, bool mla_tc = false);
+                              int num_sms, bool mla = false, bool mla_tc = false, bool mod = false);
 int decode_max_batch();
 
 cudaError_t launch_decode_fp32(const DecodeArgs& a, cudaStream_t s);

@@ -355,3 +355,34 @@ def test_check_mode_with_many_tiles(d):
     for name, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, **how), ref[3:]):
         assert_grad_close(got.double().cpu().numpy(), want, name, fp32=True)
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,T_max,page", [(1, 1, 0), (5, 5, 0), (37, 4096, 0), (20, 64, 16)])
+def test_decode_of_many_short_sequences(T, T_max, page, dtype):
+    """More units than a chunk of 128 keys holds: chunks of at least 16 keys spread them, some cut into pieces."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, d = 9, 64, 4, 64
+    lens = [max(1, T - b % 4) for b in range(B)]
+    slopes = torch.linspace(0.0, 0.5, h_q)
+    q = _randn((B, h_q, d), dtype, 1, 3.0)
+    k, v = _randn((B, h_kv, T_max, d), dtype, 2), _randn((B, h_kv, T_max, d), dtype, 3)
+    ref = oracle.modified_attention_ref(q[:, :, None].double(), k.double(), v.double(), kv_len=lens,
+                                        q_start=[n - 1 for n in lens], softcap=20.0, slopes=slopes.numpy())
+    how = dict(kv_len=torch.tensor(lens, dtype=torch.int32).cuda(), softcap=20.0, alibi_slopes=slopes.cuda(),
+               return_lse=True)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    if page:
+        n = T_max // page
+        pool = [x.view(B, h_kv, n, page, d).transpose(1, 2).reshape(B * n, h_kv, page, d).contiguous() for x in (k, v)]
+        table = torch.arange(B * n, dtype=torch.int32).view(B, n).cuda()
+        call = lambda **x: gqa.decode_paged(q, *pool, table, **how, **x)  # noqa: E731
+    else:
+        call = lambda **x: gqa.decode(q, k, v, **how, **x)  # noqa: E731
+    need = gqa.decode_workspace_size(B, h_q, h_kv, T_max, d, dtype, 0, True)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for how_ws in (dict(), dict(ws=ws), dict(num_splits=3)):
+        o, lse = call(**how_ws)
+        _check(o[:, :, None], lse[..., None], ref, dtype, str(how_ws))
+    assert gqa.get_device_error() == 0
