@@ -799,94 +799,120 @@ __global__ void __launch_bounds__(256) kv_weights_join_kernel(const __grid_const
 }
 
 // =============================================================================================
-// fp32 check mode: 128 keys per block, one per thread; kF32Rows query rows at a time (8, 16 or 32: the least that
-// holds a group's rows, else 32). Keys come in 32 columns at a time, a warp to a row, 16 rows in flight.
-// Measured: 64 heads, 35 rows over 845 keys, d = 96: 55 us; one row over 2000 keys, d = 128: 23 us (113 and 86 us
-// with each thread reading its own key's elements).
+// fp32 check mode: 128 keys per block, kGroups threads to a key, each with kRows query rows at a time (8, 16 or 32
+// rows and one group where those hold the KV head's rows; else 32 rows and 2 or 4 groups, which share the keys' loads
+// and give the few blocks of a short cache enough warps). Keys come in 32 columns at a time, a warp to a row. Rows that see no
+// key of the block are passed over 32 kGroups at a time.
+// Measured: 64 heads, 35 rows over 845 keys, d = 96: 41 us; one row over 2000 keys, d = 128: 24 us (113 and 86 us
+// with each thread reading its own key's elements, 16 rows at a time); 9 x 4 heads, 184 rows over 77 keys: 47 us
+// (74 us with one group).
 // =============================================================================================
 constexpr int kF32Cols = 32;
 
-template <int kF32Rows>
-__global__ void __launch_bounds__(128) kv_weights_fp32_kernel(WArgs a, const float* q, const float* k, int D,
-                                                              float scale) {
+template <int kRows, int kGroups>
+__global__ void __launch_bounds__(kBK * kGroups) kv_weights_fp32_kernel(WArgs a, const float* q, const float* k, int D,
+                                                                        float scale) {
+  constexpr int kAll = kRows * kGroups;   // query rows under way
+  constexpr int kPer = 32 / kGroups;      // rows of the key tile a warp loads
+  constexpr int kFly = kPer < 16 ? kPer : 16;
   __shared__ float ks[kF32Cols][kBK + 1];
-  __shared__ __align__(16) float qsm[kF32Cols][kF32Rows];
+  __shared__ __align__(16) float qsm[kF32Cols][kAll];
   __shared__ long long s_row[kBK];  // this block's cache rows (-1: not a cached key)
-  __shared__ float ls[kF32Rows];
-  __shared__ int ps[kF32Rows];
+  __shared__ float ls[kAll], part[kGroups][kBK];
+  __shared__ int ps[kAll];
+  __shared__ bool s_on[kGroups];  // the group's rows see any of the keys
   const int kt = blockIdx.x, g = blockIdx.y % a.h_kv, b = blockIdx.y / a.h_kv;
-  const int k0 = kt * kBK, key = k0 + threadIdx.x;
+  const int t = threadIdx.x % kBK, grp = threadIdx.x / kBK;
+  const int k0 = kt * kBK, key = k0 + t;
   const int kv = a.kv_len ? a.kv_len[b] : a.T_max;
   const int qs = a.q_start ? a.q_start[b] : kv - a.S_q;
   const bool valid = kv >= 1 && kv <= a.T_max && qs >= 0;
   if (!valid && kt == 0 && g == 0 && threadIdx.x == 0)
     set_device_error(a.err, kv < 1 || kv > a.T_max ? GQA_DEVERR_KV_LEN : GQA_DEVERR_POSITION);
   const long long bg = (long long)b * a.h_kv + g;
-  long long row = -1;  // this thread's key
-  if (valid && key < kv) {
-    row = bg * a.T_max + key;
-    if (a.block_table) {
-      int page = a.block_table[(long long)b * a.max_pages + key / a.page_size];
-      if (page < 0 || page >= a.num_pages) {
-        set_device_error(a.err, GQA_DEVERR_PAGE);
-        page = 0;
+  const bool cached = valid && key < kv;
+  if (grp == 0) {
+    long long row = -1;
+    if (cached) {
+      row = bg * a.T_max + key;
+      if (a.block_table) {
+        int page = a.block_table[(long long)b * a.max_pages + key / a.page_size];
+        if (page < 0 || page >= a.num_pages) {
+          set_device_error(a.err, GQA_DEVERR_PAGE);
+          page = 0;
+        }
+        row = ((long long)page * a.h_kv + g) * a.page_size + key % a.page_size;
       }
-      row = ((long long)page * a.h_kv + g) * a.page_size + key % a.page_size;
     }
+    s_row[t] = row;
   }
-  s_row[threadIdx.x] = row;
-  const bool cached = row >= 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int reach = a.window > 0 ? a.window : 0x7fffffff;
+  const int k_end = min(k0 + kBK, kv);
   float sum = 0.f, comp = 0.f;
   if (valid && k0 < kv) {
     const long long rows = (long long)a.r * a.S_q, q0 = ((long long)b * a.h_q + (long long)g * a.r) * a.S_q;
-    for (long long r0 = 0; r0 < rows; r0 += kF32Rows) {
-      float acc[kF32Rows];
-#pragma unroll
-      for (int i = 0; i < kF32Rows; ++i) acc[i] = 0.f;
-      for (int c0 = 0; c0 < D; c0 += kF32Cols) {
-        __syncthreads();
-        if (r0 == 0 || D > kF32Cols) {  // one group of columns stays for all rows
-#pragma unroll 1
-          for (int j0 = 0; j0 < kBK / 4; j0 += 16) {
-            float x[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const long long at = s_row[4 * (j0 + u) + warp];
-              x[u] = at >= 0 && c0 + lane < D ? __ldg(k + at * D + c0 + lane) : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < 16; ++u) ks[lane][4 * (j0 + u) + warp] = x[u];
-          }
-        }
-        for (int e = threadIdx.x; e < kF32Rows * kF32Cols; e += 128) {
-          const int i = e / kF32Cols, c = e - i * kF32Cols;
-          qsm[c][i] = r0 + i < rows && c0 + c < D ? q[(q0 + r0 + i) * D + c0 + c] : 0.f;
-        }
-        if (c0 == 0 && threadIdx.x < kF32Rows) {
-          const long long rr = r0 + threadIdx.x;
-          const float l = rr < rows ? a.lse[q0 + rr] : -INFINITY;
-          const long long pos = (long long)qs + rr % a.S_q;
-          ls[threadIdx.x] = l;
-          ps[threadIdx.x] = l == -INFINITY || l != l ? -1 : a.causal ? (int)min(pos, (long long)kFar) : kFar;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int c = 0; c < kF32Cols; ++c) {
-          const float kc = ks[c][threadIdx.x];
-#pragma unroll
-          for (int i = 0; i < kF32Rows; ++i) acc[i] = fmaf(kc, qsm[c][i], acc[i]);
+    for (long long r0 = 0; r0 < rows; r0 += kAll) {
+      bool sees = false;
+      __syncthreads();  // the rows before are done with
+      if (threadIdx.x < kAll) {
+        const long long rr = r0 + threadIdx.x;
+        const float l = rr < rows ? a.lse[q0 + rr] : -INFINITY;
+        const long long pos = (long long)qs + rr % a.S_q;
+        const int at = l == -INFINITY || l != l ? -1 : a.causal ? (int)min(pos, (long long)kFar) : kFar;
+        ls[threadIdx.x] = l;
+        ps[threadIdx.x] = at;
+        sees = at >= k0 && at - (k_end - 1) < reach;
+        if constexpr (kGroups > 1) {  // 32 rows: a warp to a group
+          const bool any = __any_sync(0xffffffffu, sees);
+          if (lane == 0) s_on[warp] = any;
         }
       }
-      const int reach = a.window > 0 ? a.window : 0x7fffffff;
+      if (!__syncthreads_or(sees)) continue;
+      float acc[kRows];
 #pragma unroll
-      for (int i = 0; i < kF32Rows; ++i) {
-        if (key > ps[i] || ps[i] - key >= reach) continue;
-        const float y = expf(fmaf(acc[i], scale, -ls[i])) - comp, tot = sum + y;
+      for (int i = 0; i < kRows; ++i) acc[i] = 0.f;
+      for (int c0 = 0; c0 < D; c0 += kF32Cols) {
+        if (c0 > 0) __syncthreads();
+#pragma unroll 1
+        for (int j0 = 0; j0 < kPer; j0 += kFly) {
+          float x[kFly];
+#pragma unroll
+          for (int u = 0; u < kFly; ++u) {
+            const long long at = s_row[4 * kGroups * (j0 + u) + warp];
+            x[u] = at >= 0 && c0 + lane < D ? __ldg(k + at * D + c0 + lane) : 0.f;
+          }
+#pragma unroll
+          for (int u = 0; u < kFly; ++u) ks[lane][4 * kGroups * (j0 + u) + warp] = x[u];
+        }
+        for (int e = threadIdx.x; e < kAll * kF32Cols; e += kBK * kGroups) {
+          const int i = e / kF32Cols, c = e - i * kF32Cols;
+          qsm[c][i] = r0 + i < rows && c0 + c < D ? __ldg(q + (q0 + r0 + i) * D + c0 + c) : 0.f;
+        }
+        __syncthreads();
+        if (kGroups > 1 && !s_on[grp]) continue;
+#pragma unroll 4
+        for (int c = 0; c < kF32Cols; ++c) {
+          const float kc = ks[c][t];
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) acc[i] = fmaf(kc, qsm[c][grp * kRows + i], acc[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int at = ps[grp * kRows + i];
+        if (key > at || at - key >= reach) continue;
+        const float y = expf(fmaf(acc[i], scale, -ls[grp * kRows + i])) - comp, tot = sum + y;
         comp = (tot - sum) - y;
         sum = tot;
       }
     }
+  }
+  if constexpr (kGroups > 1) {  // the groups' sums, in their order
+    part[grp][t] = sum;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k_ = 1; k_ < kGroups; ++k_) sum += part[k_][t];
   }
   if (key >= a.T_max) return;
   float* dst = a.w + bg * a.T_max + key;
@@ -1042,9 +1068,13 @@ cudaError_t launch_kv_weights_fp32(const KvWeightsArgs& a, cudaStream_t s) {
   const long long bg = (long long)a.B * a.h_kv;
   if (bg > 65535) return cudaErrorInvalidConfiguration;
   const long long rows = (long long)(a.h_q / a.h_kv) * a.S_q;
-  auto kern = rows <= 8 ? kw::kv_weights_fp32_kernel<8> : rows <= 16 ? kw::kv_weights_fp32_kernel<16>
-                                                                     : kw::kv_weights_fp32_kernel<32>;
-  kern<<<dim3((a.T_max + kw::kBK - 1) / kw::kBK, (unsigned)bg), 128, 0, s>>>(
+  const int groups = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+  auto kern = rows <= 8    ? kw::kv_weights_fp32_kernel<8, 1>
+              : rows <= 16 ? kw::kv_weights_fp32_kernel<16, 1>
+              : rows <= 32 ? kw::kv_weights_fp32_kernel<32, 1>
+              : rows <= 64 ? kw::kv_weights_fp32_kernel<32, 2>
+                           : kw::kv_weights_fp32_kernel<32, 4>;
+  kern<<<dim3((a.T_max + kw::kBK - 1) / kw::kBK, (unsigned)bg), kw::kBK * groups, 0, s>>>(
       w, reinterpret_cast<const float*>(a.q), reinterpret_cast<const float*>(a.k), a.d_h, a.scale);
   return cudaGetLastError();
 }
