@@ -318,9 +318,11 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  *   key_range  row i of sequence b sees only keys lo <= j < hi, (lo, hi) = key_range[b, i], within what the causal
  *              mask, window and length leave. It writes a document mask (lo, hi the document's rows), a
  *              bidirectional prefix (causal 0, hi the later of p + 1 and the prefix's end), or both. Rows
- *              need no order. lo < 0 means 0. A row without a key is written as zeros, lse = -inf, gradients 0, and is no error. K
- *              and V rows outside the keys that a 128-row tile's rows see between them may hold anything.
- *              bf16 prefill and backward work through the blocks between a tile's least and largest key.
+ *              need no order. lo < 0 means 0. A row without a key is written as zeros, lse = -inf, gradients 0, and is no error.
+ *              bf16 prefill and backward take the rows by tiles (128 rows: adjacent positions of the group's heads) and
+ *              work through the blocks between a tile's least and largest key. K and V rows that lie between those of
+ *              no tile (padding between or behind packed documents) may hold anything. The others have to be finite:
+ *              a row reads the keys of its tile, and of the tile beside it, with weight 0 where it does not see them.
  * mod NULL, or nothing set in it: the plain call, bit for bit.
  * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
  * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. Calls that share a workspace must

@@ -183,8 +183,18 @@ struct Work {
   int nb[kTiles];    // blocks chain t visits: pair mode j0 .. j0 + nb[t] - 1 (nb[0] <= nb[1]);
                      // split mode j0 + t, j0 + t + 2, ... (nb[0] >= nb[1])
   int nbmax;         // K/V blocks the item loads
-  int lo_key, hi_key;  // kMod: keys [lo_key, hi_key) that some row of the item sees
+  int lo_key, hi_key;  // kMod: keys from the least to the largest that some row of the item sees
+  int gap_lo, gap_hi;  // kMod: keys [gap_lo, gap_hi) between those of the two tiles (none when gap_lo >= gap_hi)
   bool valid;
+  // kMod: key lies outside both tiles' [least, largest] keys, so no row of the item sees it
+  __device__ __forceinline__ bool unseen(int key) const {
+    return key < lo_key || key >= hi_key || (key >= gap_lo && key < gap_hi);
+  }
+  // kMod: some of the N keys from key0 on is unseen
+  template <int N>
+  __device__ __forceinline__ bool any_unseen(int key0) const {
+    return key0 < lo_key || key0 + N > hi_key || max(key0, gap_lo) < min(key0 + N, gap_hi);
+  }
   // nb[t] for a chain index known only at run time. (A run-time index into a struct's array puts
   // the struct in local memory, which the shared-memory carve-out leaves almost no L1 for: the
   // roles' per-item bookkeeping measured over a microsecond per item that way.)
@@ -223,6 +233,7 @@ __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
   for (int t = 0; t < kTiles; ++t) w.nb[t] = 0;
   w.lo_key = 0;
   w.hi_key = w.kv;
+  w.gap_lo = w.gap_hi = 0;
   if (!w.valid) return w;
   if constexpr (kMod) {
     // the keys each tile's rows see, by their ranges, positions and window, and the blocks that hold them
@@ -252,6 +263,10 @@ __device__ __forceinline__ Work make_work(const PArgs& a, int idx) {
       w.hi_key = max(w.hi_key, hi[t]);
     }
     if (w.hi_key == 0) w.lo_key = 0;
+    if (hi[0] > 0 && hi[1] > 0) {
+      w.gap_lo = min(hi[0], hi[1]);
+      w.gap_hi = max(lo[0], lo[1]);
+    }
     w.j0 = w.lo_key / kBN;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) w.nb[t] = hi[t] > 0 ? (hi[t] + kBN - 1) / kBN - w.j0 : 0;
@@ -601,20 +616,20 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
         }
       }
       tc::wait_st();
-      // V rows at or past kv_len, and (sliding window) rows below the item's earliest window,
-      // get weight 0 for every row but may hold anything (NaN included), so they are zeroed in
+      // V rows at or past kv_len, (sliding window) rows below the item's earliest window, and kMod rows outside the
+      // keys of both tiles get weight 0 for every row but may hold anything (NaN included), so they are zeroed in
       // shared memory before this chain's O += P V may read them, and 0 * V stays 0. In pair mode
       // both tiles zero them (the two chains' MMAs are not ordered); a second write stores the
       // same zeros.
       const int bkey0 = (w.j0 + j) * kBN;
-      const bool zero_tail = bkey0 + kBN > (kMod ? w.hi_key : w.kv);
-      const bool zero_head = kMod ? bkey0 < w.lo_key : kWin && j == 0 && (long long)bkey0 < item_pos_min - win + 1;
-      if (ok && (zero_tail || zero_head)) {
+      const bool zero_tail = bkey0 + kBN > w.kv;
+      const bool zero_head = kWin && j == 0 && (long long)bkey0 < item_pos_min - win + 1;
+      if (ok && (kMod ? w.any_unseen<kBN>(bkey0) : zero_tail || zero_head)) {
         const int jg = J0 + j;  // block count over the CTA's items
         const int vs = jg % kVStages;
         if (wait_bar(bar(kBarVFull + vs), (uint32_t)((jg / kVStages) & 1), abort, a.err)) {
           const long long key = (long long)bkey0 + row;  // thread `row` owns V row `row` of the block
-          const bool none = kMod ? key >= w.hi_key || key < w.lo_key
+          const bool none = kMod ? w.unseen((int)key)
                                  : (zero_tail && key >= w.kv) || (zero_head && key <= item_pos_min - win);
           if (row < kBN && none) {
 #pragma unroll

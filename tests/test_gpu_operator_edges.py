@@ -1,0 +1,65 @@
+"""Edges of the operators around the cache, on the GPU: memory that may hold anything, flags, capped scores at the ends
+of their range, captured calls, copies with odd shapes. Tolerances: those of the operators' own tests."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from _tol import assert_grad_close
+
+pytestmark = pytest.mark.gpu
+
+
+def _randn(shape, dtype, seed, std=1.0):
+    return (std * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+def _forward_close(o, lse, ref, what=""):
+    """bf16: two roundings of at most 2^-8 (of the output, and of the probabilities against |v|), the rest fp32."""
+    ro, rl, mag = ref[:3]
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    tol = 2.0 ** -8 * (np.abs(ro) + mag) + 2e-4 * mag
+    assert (np.abs(o - ro) <= tol).all(), (what, np.abs(o - ro).max())
+    assert (np.isneginf(lse) == np.isneginf(rl)).all(), what
+    seen = np.isfinite(rl)
+    assert np.abs(lse[seen] - rl[seen]).max(initial=0) <= 1e-4, what
+
+
+# Keys that a tile of 128 rows sees, for the two tiles that one item holds (one head a KV head, more items than SMs),
+# and the rows of K and V that neither sees.
+GAPS = {"padding between documents": ([[0, 100]], [[130, 256]], 256), "blocks apart": ([[0, 100]], [[500, 600]], 768),
+        "later tile sees earlier keys": ([[500, 600]], [[3, 40]], 768), "first tile sees none": ([[9, 9]], [[300, 400]], 512),
+        "second tile sees none": ([[300, 400]], [[0, 0]], 512), "two documents a tile": ([[5, 60], [70, 90]], [[400, 410], [380, 390]], 512)}
+
+
+@pytest.mark.parametrize("mods", [dict(), dict(softcap=6.0), dict(slopes=True)])
+@pytest.mark.parametrize("name", list(GAPS))
+def test_rows_that_no_tile_sees_may_hold_anything(name, mods):
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h, S, d = 5, 32, 256, 64
+    first, second, T = GAPS[name]
+    rows = [first[i % len(first)] for i in range(128)] + [second[i % len(second)] for i in range(128)]
+    rg = torch.tensor(rows, dtype=torch.int32).expand(B, S, 2).contiguous()
+    q, up = _randn((B, h, S, d), torch.bfloat16, 1, 2.0), _randn((B, h, S, d), torch.bfloat16, 4)
+    k, v = _randn((B, h, T, d), torch.bfloat16, 2), _randn((B, h, T, d), torch.bfloat16, 3)
+    m = dict(mods)
+    slopes = torch.linspace(0.0, 0.3, h) if m.pop("slopes", False) else None
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), causal=False, key_range=rg.numpy(),
+                                        slopes=None if slopes is None else slopes.numpy(), d_o=up.double(), **m)
+    free = torch.ones(T, dtype=torch.bool)
+    for tile in (first, second):
+        tile = [r for r in tile if r[0] < r[1]]
+        if tile:
+            free[min(r[0] for r in tile):max(r[1] for r in tile)] = False
+    how = dict(causal=False, key_range=rg.cuda(), alibi_slopes=None if slopes is None else slopes.cuda(), **m)
+    q, up = q.cuda(), up.cuda()
+    for fill in (float("nan"), float("inf")):
+        k[:, :, free], v[:, :, free] = fill, fill
+        kd, vd = k.cuda(), v.cuda()
+        o, lse = gqa.prefill(q, kd, vd, return_lse=True, **how)
+        _forward_close(o, lse, ref, name)
+        for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, kd, vd, o, up, lse, **how), ref[3:]):
+            assert_grad_close(got.double().cpu().numpy(), want, what)
+    assert gqa.get_device_error() == 0
