@@ -969,7 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       advance(sq, w);
       if (!w.valid) set_device_error(a.err, w.kv < 1 || w.kv > a.T_max ? GQA_DEVERR_KV_LEN
                                                                         : GQA_DEVERR_POSITION);
-      else if (w.nb[0] == 0 && !(kMod && a.mod.range)) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
+      // a tile without a block (split mode: the item's only tile; kMod: either of a pair) holds rows without a key
+      else if ((w.nb[0] == 0 || (kMod && !kSplit && w.nq == 2 && w.nb[1] == 0)) && !(kMod && a.mod.range))
+        set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
       // the Q rows of every chain that runs (split mode: the one tile both chains read)
       const int zq = w.b * a.h_q + w.g * a.r + w.hb * a.H;  // first head of the block
 #pragma unroll

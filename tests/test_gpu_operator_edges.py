@@ -63,3 +63,22 @@ def test_rows_that_no_tile_sees_may_hold_anything(name, mods):
         for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, kd, vd, o, up, lse, **how), ref[3:]):
             assert_grad_close(got.double().cpu().numpy(), want, what)
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("mods", [dict(), dict(softcap=6.0), dict(slopes=True)])
+def test_a_second_tile_without_a_key_is_flagged(mods):
+    """The boundary between rows whose window holds a cached key and rows whose does not falls between the two tiles of
+    an item: flagged as in the plain call."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h, S, d, n, window = 5, 32, 256, 64, 100, 29  # row 127 sees key 99, row 128 none
+    q, k, v = (_randn((B, h, S, d), torch.bfloat16, i).cuda() for i in (1, 2, 3))
+    m = dict(mods)
+    if m.pop("slopes", False):
+        m["alibi_slopes"] = torch.linspace(0.0, 0.3, h).cuda()
+    o, lse = gqa.prefill(q, k, v, kv_len=[n] * B, window=window, return_lse=True, **m)
+    assert gqa.get_device_error() == 3
+    assert not o[:, :, 128:].any() and torch.isneginf(lse[:, :, 128:]).all() and torch.isfinite(lse[:, :, :128]).all()
+    # every row sees a key: no flag
+    gqa.prefill(q, k, v, kv_len=[n] * B, window=window + 200, return_lse=True, **m)
+    assert gqa.get_device_error() == 0
