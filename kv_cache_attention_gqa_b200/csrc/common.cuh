@@ -256,10 +256,12 @@ __device__ __forceinline__ float tanh_any(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * 2.8853900817779268f) + 1.f));
   return fmaf(-2.f, r, 1.f);
 }
-// t[k] = tanh(s[k] k1) for a thread's N scores, by the polynomial when every score of the warp is small enough (the
-// exponential unit then keeps to the softmax). Called by whole warps.
+// s[k] = tanh(s[k] k1) for a thread's N scores, by the polynomial when every score of the warp is small enough (the
+// exponential unit then keeps to the softmax). Called by whole warps. The two ways differ in the last bits, so the choice
+// must not hang on memory that may hold anything: where some score is of a key that no row sees, callers set `any` (the
+// same in the whole warp), and every score takes the way that holds for any size.
 template <int N>
-__device__ __forceinline__ void tanh_scores(float* s, float k1) {
+__device__ __forceinline__ void tanh_scores(float* s, float k1, bool any) {
   float m0 = 0.f, m1 = 0.f;
 #pragma unroll
   for (int k = 0; k < N; k += 2) {
@@ -267,7 +269,8 @@ __device__ __forceinline__ void tanh_scores(float* s, float k1) {
     m1 = fmaxf(m1, fabsf(s[k + 1]));
   }
   const float2 k2 = make_float2(k1, k1);
-  if (__all_sync(0xffffffffu, fmaxf(m0, m1) * k1 <= kTanhSmall)) {
+  // (0 times infinity is no number and not at most kTanhSmall either)
+  if (__all_sync(0xffffffffu, fmaxf(m0, m1) * (any ? INFINITY : k1) <= kTanhSmall)) {
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
       const float2 t = pair_tanh_small(pair_mul(make_float2(s[k], s[k + 1]), k2));

@@ -496,7 +496,7 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
                        (kWin && (long long)key0 <= pos_max - win);
       if constexpr (kMod) {
         need_mask = __any_sync(0xffffffffu, store_row && (key0 <= win_last || key0 + kBN - 1 > key_last));
-        if constexpr (cap) tanh_scores<kBN>(sr, a.mod.k1);
+        if constexpr (cap) tanh_scores<kBN>(sr, a.mod.k1, w.any_unseen<kBN>(key0));
         if constexpr (bias) {
           // distances key - pos from the block's first key on (exact below 2^24); under the causal mask, and where
           // the block lies on one side of every row, the bias is linear along the block
@@ -913,6 +913,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tc::tmem_relinquish();
+  }
+  if constexpr ((kMod & kModCap) != 0) {
+    // tile rows that no copy fills: scores of zero, which leave the choice in tanh_scores to the others
+    for (int i = a.H * a.P * 8 + threadIdx.x; i < kBM * 8; i += kThreads)
+#pragma unroll
+      for (int ch = 0; ch < kTiles * C::kNch; ++ch)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sQ + ch * (kBM * 128) + i * 16), "r"(0u) : "memory");
+    tc::fence_proxy_async_smem();
   }
   tc::fence_before_sync();
   cta_sync();

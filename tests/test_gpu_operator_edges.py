@@ -82,3 +82,38 @@ def test_a_second_tile_without_a_key_is_flagged(mods):
     # every row sees a key: no flag
     gqa.prefill(q, k, v, kv_len=[n] * B, window=window + 200, return_lse=True, **m)
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_capped_results_do_not_depend_on_masked_memory(d):
+    """Keys past the length, and keys that no row sees, may hold anything: the bits of the results stay the same."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S, T = 2, 6, 2, 200, 333
+    lens, start = torch.tensor([T - 40, T - 9], dtype=torch.int32), None
+    q, up = _randn((B, h_q, S, d), torch.bfloat16, 1).cuda(), _randn((B, h_q, S, d), torch.bfloat16, 4).cuda()
+    k, v = _randn((B, h_kv, T, d), torch.bfloat16, 2), _randn((B, h_kv, T, d), torch.bfloat16, 3)
+    rg = torch.tensor([[20, 250]], dtype=torch.int32).expand(B, S, 2).contiguous().cuda()
+    start = (lens - S).cuda()
+    want = None
+    for fill in (0.0, 1000.0, float("inf"), float("nan")):
+        for b, n in enumerate(lens.tolist()):
+            k[b, :, n:], v[b, :, n:] = fill, fill
+        kd, vd = k.cuda(), v.cuda()
+        # scratch of other kernels, and rows of shared memory that no query fills, differ from run to run
+        torch.full((1 << 20,), fill, device="cuda")
+        gqa.prefill(torch.full((1, 40, 300, d), 9.0 if fill else 0.1, dtype=torch.bfloat16, device="cuda"), *(
+            torch.full((1, 40, 300, d), 9.0 if fill else 0.1, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+        how = dict(q_start=start, kv_len=lens.cuda(), softcap=30.0)
+        got = list(gqa.prefill(q, kd, vd, return_lse=True, **how))
+        got += gqa.prefill_backward(q, kd, vd, got[0], up, got[1], **how)
+        k2, v2 = k.clone(), v.clone()
+        k2[:, :, :20], v2[:, :, :20], k2[:, :, 250:], v2[:, :, 250:] = fill, fill, fill, fill
+        k2, v2 = k2.cuda(), v2.cuda()
+        o, lse = gqa.prefill(q, k2, v2, return_lse=True, key_range=rg, **how)
+        got += [o, lse, *gqa.prefill_backward(q, k2, v2, o, up, lse, key_range=rg, **how)]
+        got += gqa.decode(q[:, :, -1].contiguous(), kd, vd, kv_len=lens.cuda(), softcap=30.0, return_lse=True)
+        if want is None:
+            want = [x.clone() for x in got]
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), (fill, [torch.equal(x, y) for x, y in zip(got, want)])
+    assert gqa.get_device_error() == 0
