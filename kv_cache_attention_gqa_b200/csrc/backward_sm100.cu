@@ -508,7 +508,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmq, const CUtensorM
       uint32_t pp[16], pd[16];
       const bool cap = kMod && a.mod.cap2 > 0.f;
       float* const sf = reinterpret_cast<float*>(sv);
-      if (cap) tanh_scores<32>(sf, a.mod.k1, ranged || k0 + kBK > kv);
+      if (cap) tanh_scores<32>(sf, a.mod.k1, ranged || k0 + kBK > kv ? INFINITY : a.mod.k1);
       const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
       // kMod: bias per key of distance (base 2) of this block's head, and the distance of its first row
       // (columns on from pos0; key at or before every row, as under the causal mask: the bias falls along them)
@@ -1022,7 +1022,7 @@ __device__ __forceinline__ void dq_run(const CUtensorMap& tmq, const CUtensorMap
         uint32_t pd[16];
         const bool cap = kMod && a.mod.cap2 > 0.f;
         float* const sf = reinterpret_cast<float*>(sv);
-        if (cap) tanh_scores<32>(sf, a.mod.k1, key0 < t.lo_key || key0 + 32 > t.hi_key);
+        if (cap) tanh_scores<32>(sf, a.mod.k1, key0 < t.lo_key || key0 + 32 > t.hi_key ? INFINITY : a.mod.k1);
         const float2 c2 = cap ? make_float2(a.mod.cap2, a.mod.cap2) : make_float2(a.sl2, a.sl2);
         const float2 nl = make_float2(-lse2, -lse2), nd2 = make_float2(-dr, -dr);
         // distances key - pos of this half's keys: linear in the key on one side of the tile's rows

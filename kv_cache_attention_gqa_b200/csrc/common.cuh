@@ -250,18 +250,32 @@ __device__ __forceinline__ float2 pair_tanh_small(float2 x) {
   p = pair_fma(p, z, make_float2(0x1.fffffep-1f, 0x1.fffffep-1f));
   return pair_mul(p, x);
 }
-// Any x: 1 - 2 / (e^(2x) + 1), absolute error below 3e-7 (of values up to 1, which the cap multiplies).
-__device__ __forceinline__ float tanh_any(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * 2.8853900817779268f) + 1.f));
-  return fmaf(-2.f, r, 1.f);
+// tanh of a pair of any size: x P(z) / Q(z), z = x^2, of least maximum relative error up to kTanhMost (1.2e-7 there, with
+// fp32 rounding and the reciprocal 5.2e-7; found as above, with the values of Q from the step before in the weights), and
+// past it the value there, 1 - 3e-7. P and Q have positive coefficients only, so nothing cancels: small scores keep
+// their accuracy however large the cap is, and the result is never above 1.
+constexpr float kTanhMost = 7.8f;
+__device__ __forceinline__ float2 pair_tanh_any(float2 x) {
+  x = make_float2(fminf(fmaxf(x.x, -kTanhMost), kTanhMost), fminf(fmaxf(x.y, -kTanhMost), kTanhMost));
+  const float2 z = pair_mul(x, x);
+  float2 p = pair_fma(make_float2(0x1.866e26p-17f, 0x1.866e26p-17f), z, make_float2(0x1.8544f8p-9f, 0x1.8544f8p-9f));
+  float2 q = pair_fma(make_float2(0x1.0f40bcp-22f, 0x1.0f40bcp-22f), z, make_float2(0x1.fa2856p-13f, 0x1.fa2856p-13f));
+  p = pair_fma(p, z, make_float2(0x1.091336p-3f, 0x1.091336p-3f));
+  q = pair_fma(q, z, make_float2(0x1.8773fep-6f, 0x1.8773fep-6f));
+  p = pair_fma(p, z, make_float2(0x1.fffffcp-1f, 0x1.fffffcp-1f));
+  q = pair_fma(q, z, make_float2(0x1.d9debp-2f, 0x1.d9debp-2f));
+  q = pair_fma(q, z, make_float2(1.f, 1.f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(q.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(q.y));
+  return pair_mul(pair_mul(x, p), r);
 }
-// s[k] = tanh(s[k] k1) for a thread's N scores, by the polynomial when every score of the warp is small enough (the
-// exponential unit then keeps to the softmax). Called by whole warps. The two ways differ in the last bits, so the choice
-// must not hang on memory that may hold anything: where some score is of a key that no row sees, callers set `any` (the
-// same in the whole warp), and every score takes the way that holds for any size.
+// s[k] = tanh(s[k] k1) for a thread's N scores, by the polynomial when every score of the warp is small enough (returns
+// whether). Called by whole warps. `vote` is k1, or infinity (the same in the whole warp) for the way that holds for any
+// size. The two differ in the last bits, so the choice must not hang on memory that may hold anything: callers pass
+// infinity where some score is of a key that no row sees.
 template <int N>
-__device__ __forceinline__ void tanh_scores(float* s, float k1, bool any) {
+__device__ __forceinline__ bool tanh_scores(float* s, float k1, float vote) {
   float m0 = 0.f, m1 = 0.f;
 #pragma unroll
   for (int k = 0; k < N; k += 2) {
@@ -269,8 +283,9 @@ __device__ __forceinline__ void tanh_scores(float* s, float k1, bool any) {
     m1 = fmaxf(m1, fabsf(s[k + 1]));
   }
   const float2 k2 = make_float2(k1, k1);
-  // (0 times infinity is no number and not at most kTanhSmall either)
-  if (__all_sync(0xffffffffu, fmaxf(m0, m1) * (any ? INFINITY : k1) <= kTanhSmall)) {
+  // (zero times infinity is no number, so not at most kTanhSmall either)
+  const bool small = __all_sync(0xffffffffu, fmaxf(m0, m1) * vote <= kTanhSmall) != 0;
+  if (small) {
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
       const float2 t = pair_tanh_small(pair_mul(make_float2(s[k], s[k + 1]), k2));
@@ -279,8 +294,13 @@ __device__ __forceinline__ void tanh_scores(float* s, float k1, bool any) {
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] = tanh_any(s[k] * k1);
+    for (int k = 0; k < N; k += 2) {
+      const float2 t = pair_tanh_any(pair_mul(make_float2(s[k], s[k + 1]), k2));
+      s[k] = t.x;
+      s[k + 1] = t.y;
+    }
   }
+  return small;
 }
 
 // Barrier among `threads` threads (whole warps) on barrier `id`, aligned form: only where every

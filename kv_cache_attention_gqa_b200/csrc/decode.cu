@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(Bf16Cfg<D, MT>::kThreads, 1)
       float unit = sl2;  // base-2 score of one unit of sc
       if constexpr (kMod) {
         if (a.mod.cap2 > 0.f) {
-          tanh_scores<8>(&sc[0][0], a.mod.k1, klo < nskip || klo + 16 > nvalid);
+          tanh_scores<8>(&sc[0][0], a.mod.k1, klo < nskip || klo + 16 > nvalid ? INFINITY : a.mod.k1);
           unit = a.mod.cap2;
         }
       }

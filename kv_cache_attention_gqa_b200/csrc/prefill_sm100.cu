@@ -478,6 +478,9 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
     }
 
     float m = -INFINITY, l = 0.f;
+    // cap: k1 until one of this warp's blocks has a score past kTanhSmall, then infinity: the rest of the item keeps to
+    // the one way (a cap of 20 on scores of deviation 3, 4096 rows: 296 us, with a choice per block 348)
+    float vote = a.mod.k1;
     for (int i = 0; i < nb; ++i) {
       const int j = w.blk<kSplit>(t, i);  // block of the item (from j0)
       const int gi = I0 + i;              // the chain's block count over the CTA's items
@@ -496,7 +499,10 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
                        (kWin && (long long)key0 <= pos_max - win);
       if constexpr (kMod) {
         need_mask = __any_sync(0xffffffffu, store_row && (key0 <= win_last || key0 + kBN - 1 > key_last));
-        if constexpr (cap) tanh_scores<kBN>(sr, a.mod.k1, w.any_unseen<kBN>(key0));
+        if constexpr (cap) {
+          const bool unseen = w.any_unseen<kBN>(key0);
+          if (!tanh_scores<kBN>(sr, a.mod.k1, unseen ? INFINITY : vote) && !unseen) vote = INFINITY;
+        }
         if constexpr (bias) {
           // distances key - pos from the block's first key on (exact below 2^24); under the causal mask, and where
           // the block lies on one side of every row, the bias is linear along the block

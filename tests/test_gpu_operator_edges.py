@@ -117,3 +117,29 @@ def test_capped_results_do_not_depend_on_masked_memory(d):
             want = [x.clone() for x in got]
         assert all(torch.equal(x, y) for x, y in zip(got, want)), (fill, [torch.equal(x, y) for x, y in zip(got, want)])
     assert gqa.get_device_error() == 0
+
+
+def _capped_inputs(dtype, B, h_q, h_kv, S, d):
+    q, k, v = (_randn((B, h, S, d), dtype, i) for i, h in ((1, h_q), (2, h_kv), (3, h_kv)))
+    return q, k, v, _randn((B, h_q, S, d), dtype, 4)
+
+
+@pytest.mark.parametrize("cap", [20.0, 1e4, 1e7])
+def test_small_scores_beside_large_ones_keep_their_accuracy(cap):
+    """One key's scores reach the cap, the others are of order one: these keep their relative accuracy (a tanh formed as
+    1 - 2 / (e^2x + 1) is off by 3e-7 of the cap). The large scores are negative, so that they weigh nothing."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S, d = 1, 4, 2, 150, 64
+    q, k, v, up = _capped_inputs(torch.bfloat16, B, h_q, h_kv, S, d)
+    q[..., 0], k[..., 0] = 64.0, 0.0
+    k[:, :, 3, 0] = -2.0 * cap / 8.0 if cap > 1e3 else -256.0  # q.k scale: -2 cap and less
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), softcap=cap, d_o=up.double())
+    q, k, v, up = q.cuda(), k.cuda(), v.cuda(), up.cuda()
+    o, lse = gqa.prefill(q, k, v, softcap=cap, return_lse=True)
+    _forward_close(o[:, :, 4:], lse[:, :, 4:], [x[:, :, 4:] for x in ref[:3]])
+    for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, softcap=cap), ref[3:]):
+        assert_grad_close(got.double().cpu().numpy(), want, what)
+    o, lse = gqa.decode(q[:, :, -1].contiguous(), k, v, softcap=cap, return_lse=True)
+    _forward_close(o[:, :, None], lse[..., None], [x[:, :, -1:] for x in ref[:3]])
+    assert gqa.get_device_error() == 0
