@@ -1,6 +1,7 @@
 // Host and device pieces shared by the attention kernels with modified scores: the kernel-side arguments
 // and the launch in front of them (hulls of key ranges, row terms).
 
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -11,8 +12,11 @@ namespace gqa {
 ModArgs mod_args(const ScoreMod& m, float scale) {
   ModArgs a;
   if (m.softcap > 0.f) {
-    a.k1 = (float)((double)scale / m.softcap);
-    a.cap2 = (float)((double)m.softcap * 1.4426950408889634);
+    // within fp32 for every finite cap: cap log2 e overflows past 2.3e38 (2^100 is out of any score's reach), and
+    // scale / cap under a cap far below one, where a score of zero times infinity would be no number
+    const double cap = fmin(m.softcap, 0x1p100);
+    a.k1 = (float)fmin(scale / cap, (double)FLT_MAX);
+    a.cap2 = (float)(cap * 1.4426950408889634);
   }
   a.slopes = m.slopes;
   a.range = reinterpret_cast<const int2*>(m.range);

@@ -143,3 +143,27 @@ def test_small_scores_beside_large_ones_keep_their_accuracy(cap):
     o, lse = gqa.decode(q[:, :, -1].contiguous(), k, v, softcap=cap, return_lse=True)
     _forward_close(o[:, :, None], lse[..., None], [x[:, :, -1:] for x in ref[:3]])
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap", [1e-45, 1e-39, 1e-30, 1e30, 2.5e38, 3.4028234e38])
+def test_caps_at_the_ends_of_their_range(cap, dtype):
+    """Any finite cap above zero is allowed. A vast one changes nothing, a tiny one makes every score zero."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, S, d = 1, 4, 2, 150, 64
+    q, k, v = (_randn((B, h, S, d), dtype, i) for i, h in ((1, h_q), (2, h_kv), (3, h_kv)))
+    q[:, :, 5] = 0  # scores of exactly zero
+    up = _randn((B, h_q, S, d), dtype, 4)
+    ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), softcap=cap, d_o=up.double())
+    q, k, v, up = q.cuda(), k.cuda(), v.cuda(), up.cuda()
+    o, lse = gqa.prefill(q, k, v, softcap=cap, return_lse=True)
+    _forward_close(o, lse, ref)
+    for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, softcap=cap), ref[3:]):
+        if what == "dv" or cap > 1:
+            assert_grad_close(got.double().cpu().numpy(), want, what)
+        else:  # scores at the cap: nothing flows to q and k (a score of zero passes its gradient on)
+            assert torch.isfinite(got).all()
+    o, lse = gqa.decode(q[:, :, -1].contiguous(), k, v, softcap=cap, return_lse=True)
+    _forward_close(o[:, :, None], lse[..., None], [x[:, :, -1:] for x in ref[:3]])
+    assert gqa.get_device_error() == 0
