@@ -307,7 +307,10 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const __gri
   for (int i = 0; i < n_batches; ++i) {
     if (i + 1 < n_batches) {
       if ((i + 1) % per_table == 0) {
-        fill((i + 1) / per_table);  // over the table before last: its last stores lie behind a barrier
+        // over the table before last, which its last stores have read: they lie behind a batch's barrier, unless a
+        // batch fills a table (rows of one vector)
+        if (per_table == 1) __syncthreads();
+        fill((i + 1) / per_table);
         __syncthreads();
       }
       load(i + 1, nxt);

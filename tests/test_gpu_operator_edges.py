@@ -167,3 +167,42 @@ def test_caps_at_the_ends_of_their_range(cap, dtype):
     o, lse = gqa.decode(q[:, :, -1].contiguous(), k, v, softcap=cap, return_lse=True)
     _forward_close(o[:, :, None], lse[..., None], [x[:, :, -1:] for x in ref[:3]])
     assert gqa.get_device_error() == 0
+
+
+def _evict_case(B, h_kv, T, d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.rand(B, h_kv, T, generator=g)
+    return w, *(torch.randn(B, h_kv, T, d, generator=g).to(dtype) for _ in range(2))
+
+
+def _rows_moved(dense, out, kept):
+    out = out.clone()
+    for b in range(kept.shape[0]):
+        for h in range(kept.shape[1]):
+            at = torch.from_numpy(kept[b, h][kept[b, h] >= 0]).long()
+            out[b, h, :len(at)] = dense[b, h, at]
+    return out
+
+
+@pytest.mark.parametrize("d,dtype", [(8, torch.bfloat16), (4, torch.float32), (2, torch.bfloat16), (1, torch.float32),
+                                     (1, torch.bfloat16), (16, torch.bfloat16), (3, torch.float32)])
+def test_eviction_of_narrow_rows(d, dtype):
+    """Rows of one vector: a batch of the move fills its table of addresses, which the next but one overwrites."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_kv, T, budget = 2, 3, 20000, 9001
+    w, k, v = _evict_case(B, h_kv, T, d, dtype, d)
+    lens = [T, 15001]
+    ref, new = oracle.kv_evict_ref(w.numpy(), lens, budget, sink=3, recent=70)
+    ko, vo = torch.zeros(B, h_kv, budget, d, dtype=dtype), torch.zeros(B, h_kv, budget, d, dtype=dtype)
+    want = [_rows_moved(k, ko, ref), _rows_moved(v, vo, ref), _rows_moved(k, k, ref), _rows_moved(v, v, ref)]
+    for _ in range(5):
+        kd, vd, wd, kod, vod = k.cuda(), v.cuda(), w.cuda(), ko.cuda(), vo.cuda()
+        wo = torch.empty(B, h_kv, budget, device="cuda")
+        how = dict(kv_len=lens, sink=3, recent=70)
+        kept, n = gqa.kv_evict(kd, vd, wd, budget, k_out=kod, v_out=vod, weights_out=wo, **how)
+        assert np.array_equal(kept.cpu().numpy(), ref) and n.tolist() == new.tolist()
+        assert torch.equal(kod.cpu(), want[0]) and torch.equal(vod.cpu(), want[1])
+        gqa.kv_evict(kd, vd, wd, budget, **how)
+        assert torch.equal(kd.cpu(), want[2]) and torch.equal(vd.cpu(), want[3])
+    assert gqa.get_device_error() == 0
