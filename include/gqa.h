@@ -478,7 +478,8 @@ gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float*
  *              are left as they were.
  *   paged      pools and block table as in kv_append_paged; block_table_out NULL: in place; else a
  *              device int32 (B, max_pages_out) table of the pages written, T_out = max_pages_out *
- *              page_size: other pages, or the same ones (its first columns). No page of a sequence
+ *              page_size: each column another page, or the sequence's own page of that column (a first page that
+ *              other sequences share can be replaced this way). No page of a sequence
  *              may be written that another sequence of the call reads or writes, and a table names a page once. Rows of
  *              pages outside the pool are not moved (GQA_DEVERR_PAGE). page_size >= 1.
  *   weights    (B, h_kv, T_max) fp32; weights_out (B, h_kv, T_out): the same memory or not

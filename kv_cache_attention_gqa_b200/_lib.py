@@ -857,7 +857,7 @@ def kv_evict_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table, we
                    *, kv_len=None, sink: int = 0, recent: int = 0, block_table_out=None, weights_out=None,
                    kept=None):
     """``kv_evict`` over a paged cache: in place, or with ``block_table_out`` (B, max_pages_out) into other pages
-    of the same pools (or the first ones of each sequence)."""
+    of the same pools (each column another page, or the sequence's own page of that column)."""
     num_pages, h_kv, page_size, d = _pool_shape(k_pages, v_pages)
     _need_cuda(k_pages, v_pages)
     B = weights.shape[0]

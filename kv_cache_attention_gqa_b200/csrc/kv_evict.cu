@@ -249,10 +249,16 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(const __gri
   const int rows = kMoveThreads / slice;                  // rows a block moves at once
   const int rl = threadIdx.x / slice, c = threadIdx.x - rl * slice;
   const bool lane_ok = rl < rows && c < nc;
-  // rows [r0, r1) of this block. A move in place (onto the same rows, or by a table that begins with the sequence's
-  // own pages) has an order: its first block takes all rows.
-  const bool ordered =
-      a.in_place || (a.block_table && a.block_table_out[(long long)b * a.max_pages_out] == a.block_table[(long long)b * a.max_pages]);
+  // rows [r0, r1) of this block. A move in place (onto the same rows, or by a table that keeps any of the sequence's
+  // own pages in its column) has an order: its first block takes all rows.
+  bool ordered = a.in_place;
+  if (!ordered && a.block_table) {
+    const int32_t* from = a.block_table + (long long)b * a.max_pages;
+    const int32_t* to = a.block_table_out + (long long)b * a.max_pages_out;
+    bool same = false;
+    for (int c_ = threadIdx.x; c_ < (len + a.page_size - 1) / a.page_size; c_ += kMoveThreads) same |= from[c_] == to[c_];
+    ordered = __syncthreads_or(same) != 0;
+  }
   const int per = ordered ? (part == 0 ? len : 0) : (len + row_split - 1) / row_split;
   const int r0 = ordered ? 0 : min(len, part * per), r1 = min(len, r0 + per);
   // Source and destination rows, a table of kTable at a time (dst < 0: not moved). Every thread of a row

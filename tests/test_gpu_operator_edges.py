@@ -206,3 +206,40 @@ def test_eviction_of_narrow_rows(d, dtype):
         gqa.kv_evict(kd, vd, wd, budget, **how)
         assert torch.equal(kd.cpu(), want[2]) and torch.equal(vd.cpu(), want[3])
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("fresh", [[0], [1], [0, 2], [0, 1, 2, 3, 5]])
+@pytest.mark.parametrize("page", [16, 7])
+def test_eviction_into_new_and_own_pages(fresh, page):
+    """A table that replaces some of a sequence's pages and keeps the others: the move keeps its order."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_kv, d, n = 1, 2, 64, 300
+    T, budget = n * page, 60 * page - 3
+    m = 60
+    w, k, v = _evict_case(B, h_kv, T, d, torch.bfloat16, page)
+    ref, _ = oracle.kv_evict_ref(w.numpy(), [T], budget, recent=9)
+    order = torch.randperm(n + m, generator=torch.Generator().manual_seed(3))
+    table = order[:n].view(B, n)
+    out = table[:, :m].clone()
+    out[0, fresh] = order[n:n + len(fresh)]
+
+    def pool(dense):
+        p = torch.zeros(n + m, h_kv, page, d, dtype=torch.bfloat16)
+        p[table.reshape(-1)] = dense.view(B, h_kv, n, page, d).transpose(1, 2).reshape(n, h_kv, page, d)
+        return p
+
+    kp, vp = pool(k), pool(v)
+    for _ in range(3):
+        kd, vd = kp.cuda(), vp.cuda()
+        wo = torch.empty(B, h_kv, m * page, device="cuda")
+        kept, _ = gqa.kv_evict_paged(kd, vd, table.int().cuda(), w.cuda(), budget, kv_len=[T], recent=9,
+                                     block_table_out=out.int().cuda(), weights_out=wo)
+        assert np.array_equal(kept.cpu().numpy(), ref)
+        for got, before, dense in ((kd, kp, k), (vd, vp, v)):
+            want = before.clone()
+            rows = before[out.reshape(-1)].view(B, m, h_kv, page, d).transpose(1, 2).reshape(B, h_kv, m * page, d)
+            rows = _rows_moved(dense, rows, ref)
+            want[out.reshape(-1)] = rows.view(B, h_kv, m, page, d).transpose(1, 2).reshape(m, h_kv, page, d)
+            assert torch.equal(got.cpu(), want)
+    assert gqa.get_device_error() == 0
