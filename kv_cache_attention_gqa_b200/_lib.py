@@ -314,14 +314,18 @@ def decode_workspace_size(B: int, h_q: int, h_kv: int, T_max: int, d_h: int, dty
     return n
 
 
-def _decode_workspace(ws, need: int, device, mod):
-    """A decode's workspace and its size: the caller's, or the stream's cached one. A captured call with modified
-    scores takes zeros from the capture's own pool, so that graphs captured on one stream can run at once and a
-    cached workspace that grows later takes nothing from them."""
+_HEADER = 256  # bytes of a decode workspace that have to start at zero (the ticket counter's)
+
+
+def _decode_workspace(ws, need: int, device):
+    """A decode's workspace and its size: the caller's, or the stream's cached one. A captured call takes one from the
+    capture's own pool and clears its counters in the graph (a caller's ``ws`` saves that step), so that graphs captured
+    on one stream can run at once, in any order, and a cached workspace that grows later takes nothing from them."""
     if ws is not None:
         return ws, _ws_bytes(ws)
-    if mod is not None and torch.cuda.is_current_stream_capturing():
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws[:_HEADER].zero_()
     else:
         ws = workspace(need, device)
     return ws, ws.numel()
@@ -371,7 +375,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *, kv_
     need = _ws_sizes.get(key)
     if need is None:
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits, mod is not None)
-    ws, nws = _decode_workspace(ws, need, q.device, mod)
+    ws, nws = _decode_workspace(ws, need, q.device)
     if mod is not None:
         _check("gqa_decode_mod", _lib.gqa_decode_mod(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), mod, B, h_q, h_kv, T_max,
@@ -452,7 +456,7 @@ def decode_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     need = _ws_sizes.get(key)
     if need is None:
         need = _ws_sizes[key] = decode_workspace_size(B, h_q, h_kv, T_max, d_h, q.dtype, num_splits, mod is not None)
-    ws, nws = _decode_workspace(ws, need, q.device, mod)
+    ws, nws = _decode_workspace(ws, need, q.device)
     if mod is not None:
         _check("gqa_decode_paged_mod", _lib.gqa_decode_paged_mod(
             _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), _ptr(bt), mod, B, h_q,
@@ -551,11 +555,10 @@ def mla_decode(q: torch.Tensor, cache: torch.Tensor, d_v: int = 512, *, kv_len=N
         if need == 0:
             raise GQAError("gqa_mla_decode_workspace_size", 1)
         _ws_sizes[key] = need
-    if ws is None:
-        ws = workspace(need, q.device)
+    ws, nws = _decode_workspace(ws, need, q.device)
     _check("gqa_mla_decode", _lib.gqa_mla_decode(
         _ptr(q), _ptr(cache), _ptr(out), _ptr(lse), _ptr(kl), _ptr(qp), B, h_q, T_max, d_qk, d_v,
-        scale, dt, _ptr(ws), _ws_bytes(ws), num_splits, _stream()))
+        scale, dt, _ptr(ws), nws, num_splits, _stream()))
     return (out, lse) if return_lse else out
 
 

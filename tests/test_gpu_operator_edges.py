@@ -243,3 +243,52 @@ def test_eviction_into_new_and_own_pages(fresh, page):
             want[out.reshape(-1)] = rows.view(B, h_kv, m, page, d).transpose(1, 2).reshape(m, h_kv, page, d)
             assert torch.equal(got.cpu(), want)
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["contiguous", "paged", "fp32", "mla", "mla 128 heads", "many splits"])
+def test_two_captured_plain_decodes_at_once(kind):
+    """Two graphs captured on one stream, the second replayed first, then both together on two streams: neither uses the
+    other's partial results or counters, also after the stream's own workspace has grown."""
+    import kv_cache_attention_gqa_b200 as gqa
+    from kv_cache_attention_gqa_b200 import _lib
+
+    side = torch.cuda.Stream()
+    calls = []
+    cached = dict(_lib._ws_cache)
+    for seed in (1, 10):
+        rand = lambda shape, i, dtype=torch.bfloat16: _randn(shape, dtype, seed + i).cuda()  # noqa: E731
+        if kind.startswith("mla"):
+            h = 128 if "128" in kind else 16
+            q, cache = rand((4, h, 576), 0), rand((4, 3000, 576), 1)
+            call = lambda q=q, cache=cache: gqa.mla_decode(q, cache, scale=0.05, return_lse=True)  # noqa: E731
+        elif kind == "paged":
+            q, k, v = rand((4, 8, 128), 0), rand((800, 2, 16, 128), 1), rand((800, 2, 16, 128), 2)
+            table = torch.arange(800, dtype=torch.int32).view(4, 200).cuda()
+            call = lambda q=q, k=k, v=v, t=table: gqa.decode_paged(q, k, v, t, return_lse=True)  # noqa: E731
+        else:
+            dtype = torch.float32 if kind == "fp32" else torch.bfloat16
+            q, k, v = rand((4, 8, 128), 0, dtype), rand((4, 2, 3000, 128), 1, dtype), rand((4, 2, 3000, 128), 2, dtype)
+            splits = 600 if kind == "many splits" else 0  # more chunks than blocks: drawn from the counter
+            call = lambda q=q, k=k, v=v, s=splits: gqa.decode(q, k, v, num_splits=s, return_lse=True)  # noqa: E731
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = call()
+        calls.append((graph, got, call))
+    assert _lib._ws_cache.keys() == cached.keys()  # a capture leaves the streams' workspaces alone
+    with torch.cuda.stream(side):
+        gqa.workspace(1 << 27, "cuda").fill_(0)
+    torch.cuda.synchronize()
+    calls[1][0].replay()
+    torch.cuda.synchronize()
+    wants = [call() for _, _, call in calls]
+    assert all(torch.equal(a, b) for a, b in zip(calls[1][1], wants[1]))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (graph, _, _) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, got, _), want in zip(calls, wants):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert gqa.get_device_error() == 0
