@@ -330,7 +330,8 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in
  * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take a
  * workspace as gqa_decode does, of gqa_decode_mod_workspace_size bytes (automatic chunks are smaller than
- * gqa_decode's). Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite.
+ * gqa_decode's). Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite, and for
+ * a key_range that is not 8-byte aligned.
  */
 typedef struct {
   float softcap;             /* > 0: cap of the scores; 0: none */

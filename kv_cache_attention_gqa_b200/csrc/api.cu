@@ -81,8 +81,12 @@ bool encode_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* d
 bool valid_scale(float s) { return isfinite(s) && s >= 0.f; }
 float resolve_scale(float s, int d) { return s == 0.f ? (float)(1.0 / sqrt((double)d)) : s; }
 
-// modified scores: a cap finite and > 0, or 0 for none
-bool valid_mod(const gqa_score_mod* m) { return !m || (isfinite(m->softcap) && m->softcap >= 0.f); }
+bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// modified scores: a cap finite and > 0, or 0 for none; key ranges are read as pairs
+bool valid_mod(const gqa_score_mod* m) {
+  return !m || (isfinite(m->softcap) && m->softcap >= 0.f && aligned(m->key_range, 8));
+}
 ScoreMod score_mod(const gqa_score_mod* m) {
   ScoreMod s;
   if (m) {
