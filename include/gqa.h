@@ -23,6 +23,8 @@
  * Conventions shared by every entry point:
  *   - All tensors are dense, row-major (C order), with the shapes given per call. Element type is
  *     bf16 (GQA_BF16) or fp32 (GQA_FP32, the check mode: scalar FFMA, no tensor cores).
+ *   - The bf16 outputs of gqa_prefill, gqa_prefill_backward and gqa_mla_decode are 16-byte aligned
+ *     (else GQA_ERR_INVALID_ARG).
  *   - Tensor pointers are DEVICE pointers on the current CUDA device. Small integer arrays
  *     (q_start, kv_len, q_pos, pos) are device int32 arrays of length B, or NULL for the default.
  *   - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream). Every call is

@@ -481,6 +481,7 @@ gqa_status gqa_prefill_mod(const void* q, const void* k_cache, const void* v_cac
     if (d_h != 64 && d_h != 128) return GQA_ERR_UNSUPPORTED;
     if ((long long)B * h_kv * T_max >= (1ll << 31) || (long long)B * h_q * S_q >= (1ll << 31))
       return GQA_ERR_UNSUPPORTED;
+    if (!aligned(o, 16)) return GQA_ERR_INVALID_ARG;  // written in 16-byte vectors
   }
   if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
   if (dtype == GQA_BF16 && mod && mod->key_range &&
@@ -572,6 +573,7 @@ gqa_status gqa_prefill_backward_mod(const void* q, const void* k_cache, const vo
   if ((long long)B * h_kv * T_max >= (1ll << 31) || (long long)B * h_q * S_q >= (1ll << 31))
     return GQA_ERR_UNSUPPORTED;
   if (!valid_mod(mod)) return GQA_ERR_INVALID_ARG;
+  if (dtype == GQA_BF16 && !(aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16))) return GQA_ERR_INVALID_ARG;
   const size_t base = gqa_prefill_backward_workspace_size(B, h_q, S_q);
   const size_t need = score_mod(mod).on() ? gqa_prefill_backward_mod_workspace_size(B, h_q, h_kv, S_q) : base;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
@@ -686,6 +688,7 @@ gqa_status gqa_mla_decode(const void* q, const void* cache, void* o, float* lse,
   if (dtype != GQA_BF16 && dtype != GQA_FP32) return GQA_ERR_INVALID_ARG;
   if (dtype == GQA_BF16 && !mla_dims_supported_bf16(d_qk, d_v)) return GQA_ERR_UNSUPPORTED;
   if (dtype == GQA_FP32 && (d_qk > 768 || d_v > 512)) return GQA_ERR_UNSUPPORTED;
+  if (dtype == GQA_BF16 && !aligned(o, 16)) return GQA_ERR_INVALID_ARG;
   if (B > decode_max_batch()) return GQA_ERR_UNSUPPORTED;
   if ((long long)B * T_max >= (1ll << 31) || (long long)B * h_q >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GQA_ERR_WORKSPACE;

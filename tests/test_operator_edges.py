@@ -38,3 +38,23 @@ def test_key_ranges_off_their_alignment_are_refused(lib, dtype):
         assert call(_mod(FAKE + 4)) == INVALID, name
         if name != "prefill" or dtype == 0:  # an aligned one gets to the next refusal, the workspace's
             assert call(_mod(FAKE + 8)) == WORKSPACE, name
+
+
+def test_bf16_outputs_off_their_alignment_are_refused(lib):
+    """They are written in vectors of 16 bytes; a view that starts inside one would fault."""
+    plain = lambda o, dtype: lib.gqa_prefill(FAKE, FAKE, FAKE, o, NULL, NULL, NULL, 1, 4, 2, 8, 8, 64, 0.0, 1, 0, dtype,  # noqa: E731
+                                             NULL)
+    assert plain(FAKE + 2, 0) == INVALID and plain(FAKE + 8, 0) == INVALID
+    mod = lambda o: lib.gqa_prefill_mod(FAKE, FAKE, FAKE, o, NULL, NULL, NULL, _mod(FAKE, 5.0), 1, 4, 2, 8, 8, 64, 0.0, 1, 0, 0,  # noqa: E731
+                                        NULL, 0, NULL)
+    assert mod(FAKE + 2) == INVALID and mod(FAKE) == WORKSPACE
+    for call in (lambda a, dtype: lib.gqa_prefill_backward(*a, NULL, NULL, 1, 4, 2, 8, 8, 64, 0.0, 1, 0, dtype, NULL, 0, NULL),
+                 lambda a, dtype: lib.gqa_prefill_backward_mod(*a, NULL, NULL, _mod(FAKE), 1, 4, 2, 8, 8, 64, 0.0, 1, 0, dtype,
+                                                               NULL, 0, NULL)):
+        for i in (6, 7, 8):  # dq, dk, dv
+            a = [FAKE] * 9
+            a[i] += 4
+            assert call(a, 0) == INVALID and call(a, 1) == WORKSPACE  # fp32 is written element by element
+        assert call([FAKE] * 9, 0) == WORKSPACE
+    mla = lambda o: lib.gqa_mla_decode(FAKE, FAKE, o, NULL, NULL, NULL, 1, 16, 64, 576, 512, 0.1, 0, NULL, 0, 1, NULL)  # noqa: E731
+    assert mla(FAKE + 2) == INVALID and mla(FAKE) == WORKSPACE
