@@ -292,3 +292,64 @@ def test_two_captured_plain_decodes_at_once(kind):
     for (_, got, _), want in zip(calls, wants):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert gqa.get_device_error() == 0
+
+
+def _odd_weights(kind, shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "equal":
+        return torch.full(shape, 0.5)
+    if kind == "ties":  # 0, 1/4, 1/2, 3/4
+        return torch.randint(0, 4, shape, generator=g) / 4
+    w = torch.randn(shape, generator=g)
+    if kind == "odd":
+        for i, x in enumerate((float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 1e-42)):
+            w[..., i::13] = x
+    return w
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal", "odd"])
+@pytest.mark.parametrize("page", [0, 16])
+def test_selection_shared_by_a_cluster(kind, page):
+    """Few long rows: four blocks share one row's keys. Equal weights across their borders, lengths just above the budget
+    (blocks without a key), at it and below it."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_kv, T, d, budget, sink, recent = 4, 2, 20000, 8, 5000, 3, 40
+    w = _odd_weights(kind, (B, h_kv, T), 3)
+    k = torch.arange(B * h_kv * T * d, dtype=torch.float32).view(B, h_kv, T, d)
+    lens = [T, budget + 1, 12345, budget]
+    ref, new = oracle.kv_evict_ref(w.numpy(), lens, budget, sink=sink, recent=recent)
+    want = _rows_moved(k, k, ref)
+    how = dict(kv_len=lens, sink=sink, recent=recent)
+    if page:
+        n = T // page
+        order = torch.randperm(B * n, generator=torch.Generator().manual_seed(1))
+        pool = torch.empty(B * n, h_kv, page, d)
+        pool[order] = k.view(B, h_kv, n, page, d).transpose(1, 2).reshape(B * n, h_kv, page, d)
+        kd, vd, wd = pool.cuda(), (pool + 0.5).cuda(), w.cuda()
+        kept, n_ = gqa.kv_evict_paged(kd, vd, order.view(B, n).int().cuda(), wd, budget, **how)
+        kd, vd = (x.cpu()[order].view(B, n, h_kv, page, d).transpose(1, 2).reshape(B, h_kv, T, d) for x in (kd, vd))
+    else:
+        kd, vd, wd = k.cuda(), (k + 0.5).cuda(), w.cuda()
+        kept, n_ = gqa.kv_evict(kd, vd, wd, budget, **how)
+    assert np.array_equal(kept.cpu().numpy(), ref) and n_.tolist() == new.tolist()
+    assert torch.equal(kd.cpu(), want) and torch.equal(vd.cpu(), want + 0.5)
+    assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+def test_selection_of_rows_too_long_for_shared_memory(kind):
+    """So many rows that each has one block, and more keys than it holds: every pass reads the weights again."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, T, budget, sink, recent = 80, 50001, 7000, 5, 100
+    w = _odd_weights(kind, (B, 1, T), 5)
+    k = torch.arange(B * T, dtype=torch.float32).view(B, 1, T, 1)
+    lens = [T - 7 * (b % 9) for b in range(B)]
+    some = [0, 1, 8, 37, 79]
+    ref, _ = oracle.kv_evict_ref(w[some].numpy(), [lens[b] for b in some], budget, sink=sink, recent=recent)
+    kd, vd, wd = k.cuda(), (k + 0.5).cuda(), w.cuda()
+    kept, new = gqa.kv_evict(kd, vd, wd, budget, kv_len=lens, sink=sink, recent=recent)
+    assert np.array_equal(kept.cpu().numpy()[some], ref) and new.tolist() == [budget] * B
+    want = _rows_moved(k, k, kept.cpu().numpy())
+    assert torch.equal(kd.cpu()[:, :, :, 0], want[:, :, :, 0]) and gqa.get_device_error() == 0
