@@ -379,7 +379,7 @@ gqa_status gqa_decode_paged_mod(const void* q, const void* k_pages, const void* 
  * Position encoding is what prefill, decode and mla_decode expect of their queries and keys; the
  * keys are rotated once, before they are cached.
  *
- *   x, out     rows of d elements, x != out or both the same memory with the same strides (in place).
+ *   x, out     rows of d elements: the same memory with the same strides (in place), or no memory in common.
  *   inv_freq   device double[d_rot / 2]: radians per position. Context scaling is in these values
  *              and in `scale` (finite; 1 for none).
  *   positions  device int32: per_token 0: (B), token t of sequence b sits at positions[b] + t;
@@ -402,7 +402,8 @@ gqa_status gqa_rope(const void* x, void* out, const double* inv_freq, const int3
  * kv_rope_append, kv_rope_append_paged - gqa_rope of a step's q and k and kv_append of k and v, in one
  * launch: q_out = rope(q); cache rows pos[b] + t of k_cache = rope(k_new), of v_cache = v_new.
  *   q (B, h_q, S_new, d_h), k_new, v_new (B, h_kv, S_new, d_h) with strides as in gqa_rope (NULL:
- *              dense); q_out dense (B, h_q, S_new, d_h), or q itself when q is dense.
+ *              dense); q_out dense (B, h_q, S_new, d_h), or q itself when q is dense; it shares no memory with
+ *              k_new or v_new.
  *   pos        device int32[B]: first cache row written, as in kv_append. The errors are kv_append's:
  *              a sequence that does not fit is not cached (GQA_DEVERR_POSITION), nor a row whose page
  *              is outside the pool (GQA_DEVERR_PAGE); its q_out is written all the same.

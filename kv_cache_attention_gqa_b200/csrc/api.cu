@@ -220,6 +220,55 @@ void rope_strides(long long* to, const int64_t* from, int B, int h, int S, int d
   for (int i = 0; i < 3; ++i) to[i] = size[i] == 1 ? 0 : from ? (long long)from[i] : dense[i];
 }
 
+// Rows of d adjacent elements at strides s over n[0] x n[1] x n[2] (s[i] = 0 where n[i] = 1): the elements' extent.
+void rows_extent(const long long* s, const int* n, int d, long long& lo, long long& hi) {
+  lo = 0;
+  hi = d;
+  for (int i = 0; i < 3; ++i) (s[i] < 0 ? lo : hi) += (n[i] - 1) * s[i];
+}
+
+// Whether two sets of rows share memory. Exact for sets of the same sizes and strides in which each dimension steps
+// over the whole of the inner ones (slices of one fused projection lie between each other's rows); sets of other
+// shapes count as sharing where their extents meet.
+bool rows_overlap(const void* x, const long long* xs, const int* xn, const void* y, const long long* ys, const int* yn,
+                  int d, long long elem) {
+  long long x0, x1, y0, y1;
+  rows_extent(xs, xn, d, x0, x1);
+  rows_extent(ys, yn, d, y0, y1);
+  const long long delta = (long long)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x));  // bytes
+  if (delta + y0 * elem >= x1 * elem || delta + y1 * elem <= x0 * elem) return false;
+  int dim[3] = {0, 1, 2};  // by stride, largest first
+  for (int i = 0; i < 3; ++i) {
+    if (xs[i] != ys[i] || xn[i] != yn[i] || xs[i] < 0) return true;
+    for (int j = i; j > 0 && xs[dim[j]] > xs[dim[j - 1]]; --j) {
+      const int t = dim[j];
+      dim[j] = dim[j - 1];
+      dim[j - 1] = t;
+    }
+  }
+  if (delta % elem != 0) return true;
+  long long inner = d;  // extent of the dimensions within
+  for (int i = 2; i >= 0; --i) {
+    const int k = dim[i];
+    if (xn[k] == 1) continue;
+    if (xs[k] < inner) return true;
+    inner += (xn[k] - 1) * xs[k];
+  }
+  // is delta within d of a sum of steps? In each dimension only the two steps around what is left can lead there.
+  for (int way = 0; way < 8; ++way) {
+    long long left = delta / elem;
+    for (int i = 0; i < 3; ++i) {
+      const long long s = xs[dim[i]], most = xn[dim[i]] - 1;
+      if (s == 0) continue;
+      long long step = left / s - (left % s < 0) + ((way >> i) & 1);
+      step = step < -most ? -most : step > most ? most : step;
+      left -= step * s;
+    }
+    if (left > -d && left < d) return true;
+  }
+  return false;
+}
+
 // Checks and fills the arguments of a rotation (rows x -> out); strides are host arrays of three, in
 // elements, or NULL for dense rows. The stride of a dimension of size 1 is never used: it is taken as
 // zero, so that it does not narrow the vectors.
@@ -250,6 +299,11 @@ gqa_status rope_args(RopeArgs& a, const void* x, void* out, const double* inv_fr
   a.interleaved = interleaved;
   a.inverse = inverse;
   a.scale = scale;
+  // in place (every row onto itself), or no memory in common
+  const int size[3] = {B, h, S};
+  const bool in_place = x == out && a.xs[0] == a.os[0] && a.xs[1] == a.os[1] && a.xs[2] == a.os[2];
+  if (h > 0 && S > 0 && !in_place && rows_overlap(x, a.xs, size, out, a.os, size, d, dtype == GQA_BF16 ? 2 : 4))
+    return GQA_ERR_INVALID_ARG;
   return GQA_OK;
 }
 
@@ -287,6 +341,11 @@ gqa_status rope_append_impl(const void* q, const void* k_new, const void* v_new,
   a.v_cache = v_cache;
   rope_strides(a.ks, ks, B, h_kv, S_new, d_h);
   rope_strides(a.vs, vs, B, h_kv, S_new, d_h);
+  const int q_size[3] = {B, h_q, S_new}, kv_size[3] = {B, h_kv, S_new};
+  const long long elem = dtype == GQA_BF16 ? 2 : 4;
+  if (h_q > 0 && (rows_overlap(k_new, a.ks, kv_size, q_out, a.os, q_size, d_h, elem) ||
+                  rows_overlap(v_new, a.vs, kv_size, q_out, a.os, q_size, d_h, elem)))
+    return GQA_ERR_INVALID_ARG;
   a.pos = pos;
   a.T_max = T_max;
   a.block_table = block_table;

@@ -353,3 +353,39 @@ def test_selection_of_rows_too_long_for_shared_memory(kind):
     assert np.array_equal(kept.cpu().numpy()[some], ref) and new.tolist() == [budget] * B
     want = _rows_moved(k, k, kept.cpu().numpy())
     assert torch.equal(kd.cpu()[:, :, :, 0], want[:, :, :, 0]) and gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rotation_between_slices_of_one_buffer(dtype):
+    """Rows that lie between each other's rows share no memory: they are rotated from one slice into another."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, S, H, d = 3, 5, 10, 64
+    f, _ = gqa.rope_frequencies(d)
+    buf = _randn((B, S, H, d), dtype, 1).cuda()
+    for lo, hi in (((0, 4), (4, 8)), ((5, 9), (1, 5)), ((0, 1), (9, 10)), ((2, 6), (2, 6))):
+        b = buf.clone()
+        x, out = (b[:, :, s[0]:s[1]].transpose(1, 2) for s in (lo, hi))
+        want = gqa.rope(x.clone(), f, [7, 0, 100])
+        assert gqa.rope(x, f, [7, 0, 100], out=out) is out
+        assert torch.equal(out, want)
+        rest = [h for h in range(H) if not hi[0] <= h < hi[1]]
+        assert torch.equal(b[:, :, rest], buf[:, :, rest])
+    # halves of the rows, halves of the tokens, one token's rows
+    wide = _randn((B, 4, S, 2 * d), dtype, 2).cuda()
+    want = gqa.rope(wide[..., :d].contiguous(), f, [1, 2, 3])
+    gqa.rope(wide[..., :d], f, [1, 2, 3], out=wide[..., d:])
+    assert torch.equal(wide[..., d:], want)
+    dense = _randn((1, 4, 6, d), dtype, 3).cuda()
+    want = gqa.rope(dense[:, :, 0::2].contiguous(), f, [4])
+    gqa.rope(dense[:, :, 0::2], f, [4], out=dense[:, :, 1::2])
+    assert torch.equal(dense[:, :, 1::2], want)
+    with pytest.raises(gqa.GQAError):
+        gqa.rope(dense[:, :, :3], f, [4], out=dense[:, :, 1:4])
+    # a fused projection of one step, appended from where it lies
+    qkv = _randn((B, S, 8, d), dtype, 4).cuda()
+    q, k, v = (qkv[:, :, a:b].transpose(1, 2) for a, b in ((0, 4), (4, 6), (6, 8)))
+    kc, vc = torch.zeros(B, 2, 16, d, dtype=dtype, device="cuda"), torch.zeros(B, 2, 16, d, dtype=dtype, device="cuda")
+    got = gqa.kv_rope_append(q, k, v, kc, vc, [0, 3, 6], f)
+    assert torch.equal(got, gqa.rope(q.contiguous(), f, [0, 3, 6])) and torch.equal(vc[1, :, 3:8], v[1])
+    assert gqa.get_device_error() == 0

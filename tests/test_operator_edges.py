@@ -58,3 +58,29 @@ def test_bf16_outputs_off_their_alignment_are_refused(lib):
         assert call([FAKE] * 9, 0) == WORKSPACE
     mla = lambda o: lib.gqa_mla_decode(FAKE, FAKE, o, NULL, NULL, NULL, 1, 16, 64, 576, 512, 0.1, 0, NULL, 0, 1, NULL)  # noqa: E731
     assert mla(FAKE + 2) == INVALID and mla(FAKE) == WORKSPACE
+
+
+def _strides(*s):
+    return (ctypes.c_int64 * 3)(*s)
+
+
+def test_rotation_onto_overlapping_rows_is_refused(lib):
+    """A block reads rows that another has rotated already, unless every row goes onto itself. (Sets that lie between
+    each other's rows are allowed: the GPU tests call those.)"""
+    x = 1 << 30
+    call = lambda out, xs=NULL, os=NULL, dtype=0, B=2, h=4, S=3: lib.gqa_rope(  # noqa: E731
+        x, out, FAKE, FAKE, 0, B, h, S, 64, 64, 0, xs, os, 0, 0, 1.0, dtype, NULL)
+    row = 64 * 2
+    for shift in (2, row, -row, 3 * row, -5 * row, 2 * 4 * 3 * row - 2, -(2 * 4 * 3 * row - 2)):
+        assert call(x + shift) == INVALID, shift
+    # a fused projection (2, 3, 10, 64): 4 query heads; out among them, shifted by one head, by one token, or across
+    fused = _strides(3 * 10 * 64, 64, 10 * 64)
+    for shift in (row, 3 * row, -row, 10 * row, (10 + 2) * row, (30 - 3) * row, 64, 7 * row):
+        assert call(x + shift, fused, fused) == INVALID, shift
+    assert call(x + row, fused, NULL) == INVALID and call(x, fused, NULL) == INVALID
+    assert call(x + 4 * 64, dtype=1) == INVALID
+    names = "q k v q_out kc vc inv_freq pos positions per_token B h_q h_kv S T d d_rot offset qs ks vs interleaved scale dtype stream"
+    args = dict(zip(names.split(), [x, 2 * x, 3 * x, 4 * x, 5 * x, 6 * x, FAKE, FAKE, NULL, 0, 2, 4, 2, 3, 16, 64, 64, 0, NULL,
+                                    NULL, NULL, 0, 1.0, 0, NULL]))
+    for change in (dict(q_out=x + row), dict(q_out=2 * x), dict(q_out=3 * x - 2 * row), dict(k=4 * x + 6 * row), dict(v=4 * x)):
+        assert lib.kv_rope_append(*(args | change).values()) == INVALID, change
