@@ -613,14 +613,17 @@ def _inv_freq(inv_freq: torch.Tensor, d: int, offset: int) -> torch.Tensor:
 
 def rope_frequencies(d_rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
                      original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                     device="cuda"):
+                     ramp: str = "turns", device="cuda"):
     """Angles per position of the d_rot / 2 pairs and the magnitude for ``rope``: (inv_freq float64
     tensor, scale). Without scaling inv_freq[i] = base ** (-2 i / d_rot) and scale = 1. For contexts
     ``factor`` times longer than ``original_length``:
     ``linear`` divides every frequency by factor; ``ntk`` raises the base so that the slowest pair is
     slowed by factor and the fastest is kept; ``yarn`` keeps pairs that turn at least beta_fast times over
     the original length, divides those that turn at most beta_slow times, blends in between, and returns
-    scale = 0.1 ln(factor) + 1."""
+    scale = 0.1 ln(factor) + 1. The blend is linear in the pair's turns (``ramp`` "turns", the method as published) or
+    in its index ("index": from the last index with at least beta_fast turns to the first with at most beta_slow, within
+    0 .. d_rot - 1; the usual code of models that ship with it). The pairs in between get other angles: take the one
+    that the model was trained with."""
     if d_rot <= 0 or d_rot % 2:
         raise ValueError("d_rot must be even and positive")
     if not (base > 0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor)):
@@ -635,8 +638,18 @@ def rope_frequencies(d_rot: int, base: float = 10000.0, *, scaling: str | None =
     elif scaling == "yarn":
         if original_length <= 0 or not beta_fast > beta_slow:
             raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow")
-        turns = original_length * f / (2.0 * math.pi)
-        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        if ramp == "turns":
+            turns = original_length * f / (2.0 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        elif ramp == "index":
+            if not (base > 1.0 and beta_slow > 0.0):
+                raise ValueError("a ramp over the index needs base > 1 and beta_slow > 0")
+            # the index at which original_length base ** (-2 i / d_rot) / (2 pi) turns are beta
+            at = [d_rot * math.log(original_length / (2.0 * math.pi * b)) / (2.0 * math.log(base)) for b in (beta_fast, beta_slow)]
+            first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), d_rot - 1)
+            keep = 1.0 - ((i - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
+        else:
+            raise ValueError(f"unknown ramp {ramp!r}: 'turns' or 'index'")
         f = f * (keep + (1.0 - keep) / factor)
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):

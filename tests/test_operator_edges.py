@@ -84,3 +84,33 @@ def test_rotation_onto_overlapping_rows_is_refused(lib):
                                     NULL, NULL, 0, 1.0, 0, NULL]))
     for change in (dict(q_out=x + row), dict(q_out=2 * x), dict(q_out=3 * x - 2 * row), dict(k=4 * x + 6 * row), dict(v=4 * x)):
         assert lib.kv_rope_append(*(args | change).values()) == INVALID, change
+
+
+@pytest.mark.parametrize("d_rot,base,factor,length", [(64, 10000.0, 4.0, 4096), (128, 500000.0, 8.0, 8192), (64, 10000.0, 40.0, 4096),
+                                                      (32, 1e6, 2.0, 32768)])
+def test_the_middle_of_the_yarn_ramps(d_rot, base, factor, length):
+    """Pair by pair in 64 bits: linear in the turns over the original length, or in the index between two whole bounds."""
+    import math
+
+    import kv_cache_attention_gqa_b200 as gqa
+
+    how = dict(scaling="yarn", factor=factor, original_length=length, device="cpu")
+    turns, s = gqa.rope_frequencies(d_rot, base, **how)
+    index, s2 = gqa.rope_frequencies(d_rot, base, ramp="index", **how)
+    assert s == s2 == 0.1 * math.log(factor) + 1.0
+    f = [base ** (-2.0 * i / d_rot) for i in range(d_rot // 2)]
+    n = [length * x / (2 * math.pi) for x in f]
+    first = max(max([i for i in range(-4 * d_rot, 4 * d_rot) if length * base ** (-2.0 * i / d_rot) / (2 * math.pi) >= 32.0]), 0)
+    last = min(min(i for i in range(-4 * d_rot, 4 * d_rot) if length * base ** (-2.0 * i / d_rot) / (2 * math.pi) <= 1.0), d_rot - 1)
+    assert 0 <= first < last and any(1.0 < x < 32.0 for x in n)
+    for i in range(d_rot // 2):
+        a = min(max((n[i] - 1.0) / 31.0, 0.0), 1.0)
+        b = 1.0 - min(max((i - first) / (last - first), 0.0), 1.0)
+        assert abs(float(turns[i]) / (f[i] * (a + (1 - a) / factor)) - 1) < 1e-12, i
+        assert abs(float(index[i]) / (f[i] * (b + (1 - b) / factor)) - 1) < 1e-12, i
+    assert float((turns / index - 1).abs().max()) > 0.01  # not the same angles
+    for bad in (dict(ramp="both"), dict(ramp="index", beta_slow=0.0)):
+        with pytest.raises(ValueError):
+            gqa.rope_frequencies(d_rot, base, **how, **bad)
+    with pytest.raises(ValueError):
+        gqa.rope_frequencies(d_rot, 1.0, ramp="index", **how)
