@@ -239,8 +239,10 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   return a & ~b;
 }
 
-// tanh of a pair with |x| <= kTanhSmall: x times a polynomial in x^2 (least maximum relative error, fitted by
-// iterated reweighting: 7.3e-8; with fp32 rounding 1.8e-7).
+// tanh of a pair with |x| <= kTanhSmall: x times a polynomial in z = x^2. Its coefficients are the fit of tanh(x) / x with
+// the least maximum relative error, by Lawson's method: least squares over points of (0, 0.6], again and again, each time
+// with the weights multiplied by the errors, until these are level (7.3e-8). Rounded to fp32 they give 9.2e-8, and 1.8e-7
+// with the roundings of the evaluation. (The first one is not 1: the error is spread over the interval.)
 constexpr float kTanhSmall = 0.6f;
 __device__ __forceinline__ float2 pair_tanh_small(float2 x) {
   const float2 z = pair_mul(x, x);
@@ -250,13 +252,19 @@ __device__ __forceinline__ float2 pair_tanh_small(float2 x) {
   p = pair_fma(p, z, make_float2(0x1.fffffep-1f, 0x1.fffffep-1f));
   return pair_mul(p, x);
 }
-// tanh of a pair of any size: x P(z) / Q(z), z = x^2, of least maximum relative error up to kTanhMost (1.2e-7 there, with
-// fp32 rounding and the reciprocal 5.2e-7; found as above, with the values of Q from the step before in the weights), and
-// past it the value there, 1 - 3e-7. P and Q have positive coefficients only, so nothing cancels: small scores keep
-// their accuracy however large the cap is, and the result is never above 1.
+// tanh of a pair of any size: x P(z) / Q(z), Q(0) = 1, the fit of tanh(x) / x over (0, kTanhMost] by the same method (least
+// squares of (P - Q tanh(x) / x), divided by the Q of the step before): 1.2e-7, with the roundings of the evaluation and
+// an ulp of the reciprocal 5.2e-7. Past kTanhMost the value there, 1 - 3e-7. P and Q have positive coefficients only, so
+// nothing cancels: small scores keep their accuracy however large the cap is, and the result is never above 1.
 constexpr float kTanhMost = 7.8f;
+__device__ __forceinline__ float within_nan(float x, float most) {  // x held to [-most, most]; NaN stays NaN
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-most));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(most));
+  return y;
+}
 __device__ __forceinline__ float2 pair_tanh_any(float2 x) {
-  x = make_float2(fminf(fmaxf(x.x, -kTanhMost), kTanhMost), fminf(fmaxf(x.y, -kTanhMost), kTanhMost));
+  x = make_float2(within_nan(x.x, kTanhMost), within_nan(x.y, kTanhMost));
   const float2 z = pair_mul(x, x);
   float2 p = pair_fma(make_float2(0x1.866e26p-17f, 0x1.866e26p-17f), z, make_float2(0x1.8544f8p-9f, 0x1.8544f8p-9f));
   float2 q = pair_fma(make_float2(0x1.0f40bcp-22f, 0x1.0f40bcp-22f), z, make_float2(0x1.fa2856p-13f, 0x1.fa2856p-13f));

@@ -389,3 +389,23 @@ def test_rotation_between_slices_of_one_buffer(dtype):
     got = gqa.kv_rope_append(q, k, v, kc, vc, [0, 3, 6], f)
     assert torch.equal(got, gqa.rope(q.contiguous(), f, [0, 3, 6])) and torch.equal(vc[1, :, 3:8], v[1])
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("large", [False, True])
+def test_nan_in_a_key_stays_visible_under_a_cap(large):
+    """A row that reads a NaN is NaN, whatever the sizes of the scores beside it; the other heads keep their bits."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h, S, d = 1, 3, 200, 64
+    q, k, v = (_randn((B, h, S, d), torch.bfloat16, i, 30.0 if large else 1.0) for i in (1, 2, 3))
+    how = dict(softcap=5.0 if large else 1000.0, return_lse=True)
+    want = gqa.prefill(q.cuda(), k.cuda(), v.cuda(), **how)
+    k[0, 2, 90, 7] = float("nan")
+    o, lse = gqa.prefill(q.cuda(), k.cuda(), v.cuda(), **how)
+    gone = torch.zeros(h, S, dtype=torch.bool)
+    gone[2, 90:] = True
+    assert torch.equal(torch.isnan(o[0]).all(-1).cpu(), gone) and torch.equal(torch.isnan(lse[0]).cpu(), gone)
+    assert torch.equal(o[0, :2], want[0][0, :2]) and torch.equal(lse[0, :2], want[1][0, :2])
+    o, _ = gqa.decode(q[:, :, -1].cuda().contiguous(), k.cuda(), v.cuda(), **how)
+    assert torch.isnan(o[0]).all(-1).tolist() == [False, False, True]
+    assert gqa.get_device_error() == 0
