@@ -114,3 +114,86 @@ def test_the_middle_of_the_yarn_ramps(d_rot, base, factor, length):
             gqa.rope_frequencies(d_rot, base, **how, **bad)
     with pytest.raises(ValueError):
         gqa.rope_frequencies(d_rot, 1.0, ramp="index", **how)
+
+
+def _tanh_coefficients(name):
+    """(first factor, addend) literals of the Horner steps of a function in common.cuh, in the order they stand."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kv_cache_attention_gqa_b200", "csrc",
+                        "common.cuh")
+    with open(path) as f:
+        body = f.read().split(f"float2 {name}(float2 x)")[1].split("\n}")[0]
+    return [float.fromhex(a) if "x" in a else float(a) for a in re.findall(r"make_float2\((-?(?:0x[0-9a-f.]+p-?\d+|1\.))f,", body)]
+
+
+def _lawson(x, n, m, steps):
+    """P (degree n) / Q (degree m, Q(0) = 1) in z = x^2 for tanh(x) / x of least maximum relative error on the points x."""
+    import numpy as np
+
+    z, f = (x / x.max()) ** 2, np.tanh(x) / x
+    w, q, best = np.ones_like(x) / len(x), np.ones_like(x), (np.inf, None)
+    for _ in range(steps):
+        a = np.concatenate([z[:, None] ** np.arange(n + 1), -f[:, None] * z[:, None] ** np.arange(1, m + 1)], 1)
+        weight = np.sqrt(w) / (f * np.abs(q))
+        c = np.linalg.lstsq(a * weight[:, None], f * weight, rcond=None)[0]
+        q = 1.0 + z[:, None] ** np.arange(1, m + 1) @ c[n + 1:]
+        off = np.abs(z[:, None] ** np.arange(n + 1) @ c[:n + 1] / q / f - 1.0)
+        if off.max() < best[0]:
+            best = (off.max(), c / np.concatenate([x.max() ** (2.0 * np.arange(n + 1)), x.max() ** (2.0 * np.arange(1, m + 1))]))
+        w = w * (off / off.max() + 1e-6)
+        w /= w.sum()
+    return best
+
+
+def _horner(c, z):
+    import numpy as np
+
+    r = np.full_like(z, np.float32(c[0]))
+    for x in c[1:]:  # a fused multiply-add: one rounding
+        r = (r.astype(np.float64) * z.astype(np.float64) + np.float64(np.float32(x))).astype(np.float32)
+    return r
+
+
+def test_the_polynomial_for_the_tanh_of_small_scores():
+    import numpy as np
+
+    p = _tanh_coefficients("pair_tanh_small")  # highest power first
+    assert len(p) == 5
+    least, fit = _lawson(0.6 * np.cos(np.linspace(0.0, np.pi / 2, 400, endpoint=False)), 4, 0, 3000)
+    assert 7.2e-8 < least < 7.4e-8
+    assert np.allclose(p[::-1], fit, rtol=1e-4, atol=0)  # the fit, up to where Lawson's steps have come
+    x = np.linspace(0.6, 0.0, 400000, endpoint=False)
+    # rounding the coefficients: half an ulp of each term, and the terms past the first add up to less than a fifth of it
+    half = 2.0 ** -24
+    assert np.abs(x * np.polyval(p, x * x) / np.tanh(x) - 1.0).max() < least + 1.3 * half
+    x = np.concatenate([x, np.logspace(-30, -2, 100000)]).astype(np.float32)
+    y = _horner(p, x * x) * x  # rounded: z (a tenth of it passes on), the last two sums (one, and a fifth), the product
+    assert np.abs(y / np.tanh(x.astype(np.float64)) - 1.0).max() < least + (1.3 + 0.1 + 1.2 + 1.0) * half
+
+
+def test_the_rational_function_for_the_tanh_of_any_score():
+    import numpy as np
+
+    c = _tanh_coefficients("pair_tanh_any")
+    # as they stand: P and Q by turns, the highest powers first; Q is one degree longer
+    p, q = [c[0], c[1], c[4], c[6]], [c[2], c[3], c[5], c[7], c[8]]
+    assert len(c) == 9 and q[-1] == 1.0 and min(c) > 0
+    t = np.linspace(0.0, np.pi / 2, 1500)[1:]
+    least, fit = _lawson(np.unique(np.concatenate([7.8 * np.sin(t), 7.8 * (1 - np.cos(t))])), 3, 4, 1500)
+    assert 1.1e-7 < least < 1.2e-7
+    ref = lambda v: np.tanh(v.astype(np.float64))  # noqa: E731
+    x = np.linspace(7.8, 0.0, 400000, endpoint=False)
+    # rounding the coefficients: no term is negative, so P and Q are each off by half an ulp at most
+    half = 2.0 ** -24
+    assert np.abs(x * np.polyval(p, x * x) / np.polyval(q, x * x) / ref(x) - 1.0).max() < least + 2 * half
+    assert np.allclose([*p[::-1], *q[-2::-1]], fit, rtol=3e-3, atol=0)
+    x = np.concatenate([np.linspace(0.0, 20.0, 400001)[1:], np.logspace(-30, 30, 200000)]).astype(np.float32)
+    v = np.minimum(x, np.float32(7.8))
+    for ulp in (-1.2e-7, 0.0, 1.2e-7):  # the reciprocal's
+        r = (1.0 / _horner(q, v * v).astype(np.float64) * (1.0 + ulp)).astype(np.float32)
+        y = v * _horner(p, v * v) * r
+        # roundings, each of half an ulp: z (three times in P, four in Q), three sums of P, four of Q, the reciprocal (and
+        # its ulp, two halves), two products
+        assert np.abs(y / ref(x) - 1.0).max() < least + (2 + 7 + 7 + 3 + 2) * half and y.max() <= 1.0
