@@ -34,7 +34,7 @@
 // 8 sequences of 8192 keys, 8 KV heads, 4 rows each, d = 128 (138 MB): 31.0 us, 4.5 TB/s; two groups of
 // eight warps taking tiles in turn: 32.8 us, so what is left is the start and the end of a launch this short.
 //
-// fp32 check mode: one thread per key, scalar FFMA.
+// fp32 check mode: up to four threads to a key, one per group of 32 query rows, scalar FFMA.
 
 #include <math.h>
 
@@ -778,7 +778,6 @@ __global__ void __launch_bounds__(SCfg<D, MT>::kThreads, 1)
 
 // The sums of the parts of each key, in their order.
 __global__ void __launch_bounds__(256) kv_weights_join_kernel(const __grid_constant__ WArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int key = blockIdx.x * 256 + threadIdx.x;
   const long long bg = blockIdx.y;
   if (key >= a.T_max) return;
