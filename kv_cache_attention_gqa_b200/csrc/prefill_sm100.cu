@@ -179,9 +179,9 @@ struct Work {
   bool split;        // split mode
   int nq;            // Q tiles loaded (pair mode: tiles with at least one query row; split: 1)
   int nt;            // chains (pair mode: nq; split mode: 2)
-  int j0;            // first K/V block of the item (> 0 only under a sliding window)
-  int nb[kTiles];    // blocks chain t visits: pair mode j0 .. j0 + nb[t] - 1 (nb[0] <= nb[1]);
-                     // split mode j0 + t, j0 + t + 2, ... (nb[0] >= nb[1])
+  int j0;            // first K/V block of the item (> 0 only under a sliding window or key ranges)
+  int nb[kTiles];    // blocks chain t visits: pair mode j0 .. j0 + nb[t] - 1 (nb[0] <= nb[1]; with key ranges either
+                     // may be the larger one, or 0); split mode j0 + t, j0 + t + 2, ... (nb[0] >= nb[1])
   int nbmax;         // K/V blocks the item loads
   int lo_key, hi_key;  // kMod: keys from the least to the largest that some row of the item sees
   int gap_lo, gap_hi;  // kMod: keys [gap_lo, gap_hi) between those of the two tiles (none when gap_lo >= gap_hi)
@@ -558,13 +558,18 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       // Pair mode: the two chains take turns on the exponential unit, chain 0 first in every
       // round; left to themselves their softmax phases overlap and share the unit, which
       // lengthens both chains. Within an item chain 1 waits for chain 0's current round and chain
-      // 0 for chain 1's previous one. Waits are by phase parity, so a barrier must not complete
-      // two phases past the one its waiter asks for. Chain 1 cannot get there on chain 0's
-      // barrier (its next round waits for chain 0's next one); chain 0's first round of an item
-      // waits for nothing, so chain 0's rounds cycle through four barriers (the K/V rings keep
-      // either chain within three rounds of the other: a block is loaded only after both chains
-      // released the one two or three before it). Chain 0 waits on a single barrier, which lags
-      // a phase when chain 1 runs two rounds behind; the wait then passes at once and chain 0
+      // 0 for chain 1's previous one, as far as both have rounds. Waits are by phase parity, so a
+      // barrier must not complete two phases past the one its waiter asks for, or the wait would
+      // not end. Chain 1 cannot get there on chain 0's barrier: its next round waits for chain
+      // 0's next one, and of its rounds past nb[0], which nothing holds, chain 0 asks for none.
+      // Chain 0's first round of an item waits for nothing, so chain 0's rounds cycle through
+      // four barriers: in the rounds that chain 1 waits for, the K/V rings keep chain 0 within
+      // three rounds of it (a block is loaded only after both chains released the one two or
+      // three before it, and chain 1 releases one of its own blocks only after its round on it).
+      // Past nb[1] chain 1's issuer releases the blocks unread and chain 0 runs on, but chain 1's
+      // next wait is in an item in which both have rounds, where the rings hold chain 0 again. A
+      // barrier that lags lets a wait pass early, which costs no more than the turn: chain 0 waits
+      // on a single one, which lags a phase when chain 1 runs two rounds behind, and then
       // runs on (holding it to chain 1's pace there measured 8% slower on prefill_4k). Split
       // mode takes no turns (4% faster on chunked prefill than taking them). The loads and the
       // row maximum run outside the turn.

@@ -409,3 +409,36 @@ def test_nan_in_a_key_stays_visible_under_a_cap(large):
     o, _ = gqa.decode(q[:, :, -1].cuda().contiguous(), k.cuda(), v.cuda(), **how)
     assert torch.isnan(o[0]).all(-1).tolist() == [False, False, True]
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_tiles_of_very_different_lengths_take_their_turns(seed):
+    """Pairs of tiles whose keys span none to 64 blocks each, in any order: the chains' turns never hold one another for
+    good (a wait that ran out would be flagged)."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h, S, T, d = 1, 16, 2560, 8192, 64
+    g = torch.Generator().manual_seed(seed)
+    rows = []
+    for tile in range(S // 128):
+        kind = int(torch.randint(0, 4, (1,), generator=g))
+        lo = int(torch.randint(0, T, (1,), generator=g))
+        hi = [lo, min(T, lo + 100), T, int(torch.randint(lo, T + 1, (1,), generator=g))][kind]
+        rows += [[0 if kind == 2 else lo, hi]] * 128
+    rg = torch.tensor(rows, dtype=torch.int32)[None].contiguous().cuda()
+    q, k, v = (_randn((B, h, n, d), torch.bfloat16, seed + i).cuda() for i, n in ((1, S), (2, T), (3, T)))
+    key = torch.arange(T, device="cuda")
+    seen = (key >= rg[0, :, :1]) & (key < rg[0, :, 1:])
+    first = None
+    for _ in range(3):
+        o, lse = gqa.prefill(q, k, v, causal=False, key_range=rg, softcap=4.0, return_lse=True)
+        assert gqa.get_device_error() == 0
+        first = (o.clone(), lse.clone()) if first is None else first
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    for a in range(0, h, 5):
+        s = 4.0 * torch.tanh(q[0, a].double() @ k[0, a].double().T / 8.0 / 4.0)
+        s = s.masked_fill(~seen, -float("inf"))
+        rl = torch.logsumexp(s, -1)
+        p = torch.exp(s - torch.where(torch.isfinite(rl), rl, 0.0)[:, None])
+        x, mag = p @ v[0, a].double(), p @ v[0, a].double().abs()
+        _forward_close(o[0, a], lse[0, a], [t.cpu().numpy() for t in (x, rl, mag)], a)
