@@ -193,12 +193,15 @@ def _scale(scale) -> float:
 # The current device's index, without torch.cuda.current_device's check that CUDA is up: for calls that have seen a
 # CUDA tensor.
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# The raw handle of a device's current stream (torch.cuda.current_stream() builds an object around it, which costs more
+# than the launch of a small kernel), and whether that stream is capturing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _stream():
-    """The raw handle of the current stream (torch.cuda.current_stream() builds an object around it, which
-    costs more than the launch of a small kernel)."""
-    return torch._C._cuda_getCurrentRawStream(_device())
+    """The raw handle of the current device's current stream."""
+    return _raw_stream(_device())
 
 
 def debug_expire_waits(enable: bool) -> None:
@@ -319,11 +322,11 @@ _HEADER = 256  # bytes of a decode workspace that have to start at zero (the tic
 
 def _decode_workspace(ws, need: int, device):
     """A decode's workspace and its size: the caller's, or the stream's cached one. A captured call takes one from the
-    capture's own pool and clears its counters in the graph (a caller's ``ws`` saves that step), so that graphs captured
+    capture's own pool and clears its counters in the graph (1 us; a caller's ``ws`` saves it), so that graphs captured
     on one stream can run at once, in any order, and a cached workspace that grows later takes nothing from them."""
     if ws is not None:
         return ws, _ws_bytes(ws)
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if _capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         ws[:_HEADER].zero_()
     else:
@@ -341,7 +344,7 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     and stream (every completed decode leaves its counter region at zero again)."""
     dev = torch.device(device)
     index = torch.cuda.current_device() if dev.index is None else dev.index
-    key = (index, torch._C._cuda_getCurrentRawStream(index))
+    key = (index, _raw_stream(index))
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:

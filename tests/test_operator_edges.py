@@ -197,3 +197,25 @@ def test_the_rational_function_for_the_tanh_of_any_score():
         # roundings, each of half an ulp: z (three times in P, four in Q), three sums of P, four of Q, the reciprocal (and
         # its ulp, two halves), two products
         assert np.abs(y / ref(x) - 1.0).max() < least + (2 + 7 + 7 + 3 + 2) * half and y.max() <= 1.0
+
+
+def test_the_binding_does_without_private_helpers_of_torch():
+    """They are shortcuts for the current device, its stream and whether that captures."""
+    import os
+    import subprocess
+    import sys
+
+    names = ["_cuda_getCurrentRawStream", "_cuda_isCurrentStreamCapturing", "_cuda_getDevice"]
+    code = f"""
+import torch
+for n in {names}:
+    if hasattr(torch._C, n):
+        delattr(torch._C, n)
+from kv_cache_attention_gqa_b200 import _lib
+assert _lib._capturing is torch.cuda.is_current_stream_capturing and _lib._device is torch.cuda.current_device
+torch.cuda.current_stream = lambda index: type("S", (), dict(cuda_stream=40 + index))
+assert _lib._raw_stream(2) == 42
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
