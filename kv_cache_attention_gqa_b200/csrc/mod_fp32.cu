@@ -249,7 +249,10 @@ __device__ __forceinline__ void rows_block(const FArgs& a, int block) {
     __syncwarp();  // a row's threads share a warp
     const float* from = kGrad ? sk : sv;
 #pragma unroll 4
-    for (int j = 0; j < kRows; ++j) axpy<NC, kLanes>(acc, sp[ty * kRows + j], from + j * kStride, tx);
+    for (int j = 0; j < kRows; ++j) {
+      const float x = sp[ty * kRows + j];
+      if (x != 0.f) axpy<NC, kLanes>(acc, x, from + j * kStride, tx);  // rows with no weight may hold anything
+    }
   }
   if (i >= a.S_q) return;
   if (!kGrad) {
@@ -335,6 +338,7 @@ __device__ __forceinline__ void keys_block(const FArgs& a) {
 #pragma unroll 4
       for (int x = 0; x < kKvQ; ++x) {
         const float p = sp[ty * kKvQ + x], ds = sds[ty * kKvQ + x];
+        if (p == 0.f && ds == 0.f) continue;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           const int c = 4 * (tx + kLanes * n);

@@ -442,3 +442,27 @@ def test_tiles_of_very_different_lengths_take_their_turns(seed):
         p = torch.exp(s - torch.where(torch.isfinite(rl), rl, 0.0)[:, None])
         x, mag = p @ v[0, a].double(), p @ v[0, a].double().abs()
         _forward_close(o[0, a], lse[0, a], [t.cpu().numpy() for t in (x, rl, mag)], a)
+
+
+def test_check_mode_reads_nothing_into_keys_without_weight():
+    """Key ranges in fp32: NaN in keys that a tile's rows span but none sees, and in queries that see no key."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    for S, T, d in ((90, 160, 40), (700, 300, 64)):
+        B, h_q, h_kv = 1, 6, 2
+        q, k, v = (_randn((B, h, n, d), torch.float32, i) for i, h, n in ((1, h_q, S), (2, h_kv, T), (3, h_kv, T)))
+        up = _randn((B, h_q, S, d), torch.float32, 4)
+        rg = torch.tensor([[0, 42] if i < 42 else [7, 7] if i < 50 else [100, 150] for i in range(S)], dtype=torch.int32)[None]
+        ref = oracle.modified_attention_ref(q.double(), k.double(), v.double(), causal=False, key_range=rg.numpy(),
+                                            softcap=8.0, d_o=up.double())
+        for x in (k, v):
+            x[:, :, 42:100], x[:, :, 150:] = float("nan"), float("inf")
+        q[:, :, 42:50], up[:, :, 42:50] = float("nan"), float("nan")
+        q, k, v, up = q.cuda(), k.cuda(), v.cuda(), up.cuda()
+        how = dict(causal=False, key_range=rg.contiguous().cuda(), softcap=8.0)
+        o, lse = gqa.prefill(q, k, v, return_lse=True, **how)
+        assert not o[:, :, 42:50].any()
+        _forward_close(o, lse, ref)
+        for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, **how), ref[3:]):
+            assert_grad_close(got.double().cpu().numpy(), want, what, fp32=True)
+        assert gqa.get_device_error() == 0
