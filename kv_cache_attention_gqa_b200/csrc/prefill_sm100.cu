@@ -716,7 +716,9 @@ __device__ __forceinline__ void softmax_role(const PArgs& a, int t, int wq, int 
       }
       const float m0 = xm[row], l0 = xm[128 + row], m1 = xm[256 + row], l1 = xm[384 + row];
       const float M = fmaxf(m0, m1);
-      const bool empty = M == -INFINITY;  // no visible key in either chain (sliding window)
+      // no visible key in either chain (sliding window); kMod: a row whose scores are all NaN has no maximum either, and
+      // stays NaN
+      const bool empty = M == -INFINITY && !(kMod && (l0 != l0 || l1 != l1));
       if (empty && store_row && t == 0 && !(kMod && a.mod.range)) set_device_error(a.err, GQA_DEVERR_NO_VISIBLE);
       const float f0 = empty || w.nb[0] == 0 ? 0.f : fast_exp2(m0 - M);
       const float f1 = empty || w.nb[1] == 0 ? 0.f : fast_exp2(m1 - M);

@@ -466,3 +466,30 @@ def test_check_mode_reads_nothing_into_keys_without_weight():
         for what, got, want in zip(("dq", "dk", "dv"), gqa.prefill_backward(q, k, v, o, up, lse, **how), ref[3:]):
             assert_grad_close(got.double().cpu().numpy(), want, what, fp32=True)
         assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("B,h", [(1, 3), (5, 32)])
+@pytest.mark.parametrize("mods", [dict(softcap=20.0), dict(slopes=True), dict(ranges=True)])
+def test_a_nan_query_gives_a_nan_row(mods, B, h):
+    """All scores of the row are NaN: it is no row without a key. Few tiles (two chains share one) and many."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    S, d = 200, 64
+    q, k, v = (_randn((B, h, S, d), torch.bfloat16, i) for i in (1, 2, 3))
+    q[0, 1, 50, 3] = float("nan")
+    how = dict(softcap=mods.get("softcap", 0.0), return_lse=True)
+    if mods.get("slopes"):
+        how["alibi_slopes"] = torch.linspace(0.0, 0.3, h).cuda()
+    if mods.get("ranges"):
+        how["key_range"] = torch.tensor([[0, S]], dtype=torch.int32).expand(B, S, 2).contiguous().cuda()
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    gone = torch.zeros(B, h, S, dtype=torch.bool, device="cuda")
+    gone[0, 1, 50] = True
+    o, lse = gqa.prefill(q, k, v, **how)
+    assert torch.equal(torch.isnan(o).all(-1), gone) and torch.equal(torch.isnan(o).any(-1), gone)
+    assert torch.equal(torch.isnan(lse), gone) and torch.isfinite(lse[~gone]).all()
+    if mods.get("ranges"):
+        how["key_range"] = how["key_range"][:, 0].contiguous()
+    o, lse = gqa.decode(q[:, :, 50].contiguous(), k, v, **how)
+    assert torch.equal(torch.isnan(o).all(-1), gone[:, :, 50]) and torch.isfinite(o[~gone[:, :, 50]]).all()
+    assert gqa.get_device_error() == 0
