@@ -494,7 +494,7 @@ gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float*
  *   kv_len     device int32[B] or NULL (= T_max); 0 <= kv_len[b] <= T_max, else the sequence is left
  *              alone, its new_len is kv_len[b] and GQA_DEVERR_KV_LEN is set.
  *   budget     1 .. T_out; sink, recent >= 0, sink + recent <= budget.
- * Any d_h >= 1. B * h_kv <= 65535, cache (or pool) rows below 2^31. Two launches in order on `stream`.
+ * Any d_h >= 1. B * h_kv <= 65535; rows of the caches, of the pool and of the weights below 2^31 - 2^16. Two launches in order on `stream`.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 gqa_status kv_evict(const void* k_cache, const void* v_cache, void* k_out, void* v_out,

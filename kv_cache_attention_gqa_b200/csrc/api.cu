@@ -431,10 +431,10 @@ gqa_status evict_impl(EvictArgs& a, int d_h, gqa_dtype dtype, void* stream) {
   if (a.w_out == a.w ? a.T_out != a.T_max
                      : overlap(a.w, bg * a.T_max * 4, a.w_out, bg * a.T_out * 4))
     return GQA_ERR_INVALID_ARG;
-  // rows are counted in 32 bits
+  // rows are counted in 32 bits, by threads that look up to a few blocks' width past the last one
+  const long long most = (1ll << 31) - (1ll << 16);
   const long long rows = a.block_table ? (long long)a.num_pages * a.h_kv * a.page_size : (long long)bg * a.T_max;
-  if (rows >= (1ll << 31) || (long long)bg * a.T_max >= (1ll << 31) || (long long)bg * a.T_out >= (1ll << 31) ||
-      (long long)bg > 65535)
+  if (rows >= most || (long long)bg * a.T_max >= most || (long long)bg * a.T_out >= most || (long long)bg > 65535)
     return GQA_ERR_UNSUPPORTED;
   a.err = device_error_ptr();
   const int sms = sm_count();

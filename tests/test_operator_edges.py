@@ -219,3 +219,15 @@ assert _lib._raw_stream(2) == 42
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr
+
+
+def test_eviction_counts_its_rows_in_32_bits(lib):
+    """Threads step past the last row, so the limit lies that far below 2^31."""
+    far, most = 1 << 44, 2**31 - 2**16
+    call = lambda T, To, budget: lib.kv_evict(far, 2 * far, 3 * far, 4 * far, 5 * far, 6 * far, 7 * far, 8 * far, 9 * far, 1, 1,  # noqa: E731
+                                              T, To, budget, 0, 0, 1, 0, NULL)
+    for T, To in ((most, 64), (2**31 - 1, 64), (64, most), (64, 2**31 - 1)):
+        assert call(T, To, 16) == UNSUPPORTED, (T, To)
+    paged = lambda max_pages, max_out: lib.kv_evict_paged(far, 2 * far, 3 * far, 4 * far, 5 * far, 6 * far, 7 * far, 8 * far,  # noqa: E731
+                                                          9 * far, 1, 1, 8, 1, max_pages, max_out, 4, 0, 0, 1, 0, NULL)
+    assert paged(most, 8) == UNSUPPORTED and paged(8, most) == UNSUPPORTED
