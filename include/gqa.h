@@ -316,7 +316,9 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * the arguments of the calls without _mod, and a gqa_score_mod (host memory, read during the call):
  *   s = scale q.k;  with a softcap c > 0:  s = c tanh(s / c);  with slopes:  s = s - slope[a] |p - j|
  * for query head a, the row's position p (q_start[b] + i, decode q_pos[b]) and the key's row j. The softmax, lse
- * and the gradients are those of the modified score; slopes are constants (they get no gradient).
+ * and the gradients are those of the modified score; slopes are constants (they get no gradient). Positions are
+ * cache rows throughout, those of window and key_range too: once kv_evict has moved rows, a distance is one between
+ * the rows that are left, not between the tokens' own positions (which the rotation alone keeps).
  *   key_range  row i of sequence b sees only keys lo <= j < hi, (lo, hi) = key_range[b, i], within what the causal
  *              mask, window and length leave. It writes a document mask (lo, hi the document's rows), a
  *              bidirectional prefix (causal 0, hi the later of p + 1 and the prefix's end), or both. Rows
@@ -324,7 +326,8 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  *              bf16 prefill and backward take the rows by tiles (128 rows: adjacent positions of the group's heads) and
  *              work through the blocks between a tile's least and largest key. K and V rows that lie between those of
  *              no tile (padding between or behind packed documents) may hold anything. The others have to be finite:
- *              a row reads the keys of its tile, and of the tile beside it, with weight 0 where it does not see them.
+ *              a row reads the keys of its tile, and of the tile beside it, with weight 0 where it does not see them. The
+ *              bf16 backward wants q and d_o finite in every row, rows without a key included.
  * mod NULL, or nothing set in it: the plain call, bit for bit.
  * gqa_prefill_mod needs a workspace (256-byte aligned, no initial contents, gqa_prefill_mod_workspace_size
  * bytes) when key_range is given and dtype is GQA_BF16; else it may be NULL. Calls that share a workspace must
@@ -332,7 +335,7 @@ gqa_status kv_append_paged(void* k_pages, void* v_pages, const void* k_new, cons
  * gqa_prefill_backward_mod_workspace_size bytes when anything is set in mod, gqa_prefill_backward's else; in
  * bf16 it forms rowsum(dO o) from the probabilities in fp32 and does not read o. The decode calls take a
  * workspace as gqa_decode does, of gqa_decode_mod_workspace_size bytes (automatic chunks are smaller than
- * gqa_decode's). Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite, and for
+ * gqa_decode's). bf16 forms the cap's tanh to 5.2e-7 relative. Errors: as the plain calls; INVALID_ARG for a cap that is negative, NaN or infinite, and for
  * a key_range that is not 8-byte aligned.
  */
 typedef struct {
@@ -444,7 +447,7 @@ gqa_status kv_rope_append_paged(const void* q, const void* k_new, const void* v_
  *   weights    (B, h_kv, T_max) fp32. accumulate 0: every entry is written, zero where no row sees
  *              the key; accumulate 1: the sums are added to entries j < kv_len[b], the others are left.
  *   q_start    device int32[B] or NULL: cache row of query row 0; NULL: the queries are the last S_q
- *              cached rows, q_start[b] = kv_len[b] - S_q.
+ *              cached rows, q_start[b] = kv_len[b] - S_q (gqa_prefill's NULL is row 0: give both calls the same).
  *   kv_len, scale, causal, window: as in gqa_prefill. A sequence whose length or start is out of
  *              range is flagged (GQA_DEVERR_KV_LEN, GQA_DEVERR_POSITION) and adds nothing.
  *   dtype      GQA_BF16: d_h 64 or 128 (tcgen05 kernel); GQA_FP32: d_h <= 256 (check mode).
@@ -475,7 +478,8 @@ gqa_status gqa_kv_weights_paged(const void* q, const void* k_pages, const float*
  *   budget - sink - recent with the largest w (ties: the lower row; NaN ranks below every number).
  * The rows that stay move to rows 0, 1, ... in their order, K, V and weights alike. Keys keep the
  * rotation they were cached with; appended tokens go to row new_len[b] on, with their own positions
- * (kv_rope_append's `positions`).
+ * (kv_rope_append's `positions`). The attention calls know rows only: a causal mask at the last row, a window,
+ * slopes and key ranges count the rows that are left (pass q_pos or q_start as rows).
  *
  *   k_cache, v_cache (B, h_kv, T_max, d_h); k_out, v_out (B, h_kv, T_out, d_h): the same memory
  *              (in place, T_out = T_max) or other, not overlapping memory. Rows past the new length

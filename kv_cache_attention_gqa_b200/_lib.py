@@ -787,7 +787,7 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, *, q_s
     """Attention weight of every cached key, fp32 (B, h_kv, T_max): the sum over the group's heads and the
     query rows that see it of exp(scale q.k - lse). q (B, h_q, S_q, d_h) with lse (B, h_q, S_q) as returned
     by ``prefill``, or (B, h_q, d_h) with (B, h_q) by ``decode``. ``q_start`` None: the queries are the
-    last S_q cached rows. ``weights`` given: the sums are added to its entries j < kv_len, in place. The scores
+    last S_q cached rows (``prefill``'s None is row 0: give both the same). ``weights`` given: the sums are added to its entries j < kv_len, in place. The scores
     are plain ones, so ``lse`` is one of a call without softcap, alibi_slopes and key_range."""
     if k_cache.dim() != 4 or k_cache.shape[0] != q.shape[0]:
         raise ValueError("k_cache must be (B, h_kv, T_max, d_h)")
@@ -846,7 +846,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     heaviest of the others (``weights`` from ``kv_weights``; ties to the lower row) move to the front in
     their order. In place, or into ``k_out``, ``v_out``, ``weights_out`` of (B, h_kv, T_out, d_h) and
     (B, h_kv, T_out). Weights past the new length become zero. Returns (kept, new_len): the rows kept
-    (B, h_kv, budget) int32, -1 past the new length, and the new lengths (B,) int32."""
+    (B, h_kv, budget) int32, -1 past the new length, and the new lengths (B,) int32. Keys keep their rotation; in the
+    calls after it ``window``, ``alibi_slopes`` and ``key_range`` count the rows that are left."""
     _need_cuda(k_cache, v_cache, k_out, v_out)
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache / v_cache must both be (B, h_kv, T_max, d_h)")

@@ -2,7 +2,8 @@
 // rows i that see key j of P = exp(scale q_{a,i} . k_j - lse_{a,i}), lse from the forward pass.
 //
 // Mathematics. Given lse the softmax needs no further statistics, so the weight of a key is a plain sum
-// over query rows of exp2(c s - lse2) with c = scale log2 e. The probabilities are never stored.
+// over query rows of exp2(c s - lse2) with c = scale log2 e. The probabilities are never stored. The exponent is one fp32
+// fused multiply-add, so a weight's relative error is that of lse2 in fp32: 2^-24 |lse2| ln 2, 7e-7 at an lse2 of 16.
 //
 // bf16, more than 32 query rows a group (prompts, windows of queries): key-stationary on the tensor cores.
 // A unit of work is 256 keys of one (sequence, KV head) against the query rows that see them (all of them,
