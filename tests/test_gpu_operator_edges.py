@@ -493,3 +493,27 @@ def test_a_nan_query_gives_a_nan_row(mods, B, h):
     o, lse = gqa.decode(q[:, :, 50].contiguous(), k, v, **how)
     assert torch.equal(torch.isnan(o).all(-1), gone[:, :, 50]) and torch.isfinite(o[~gone[:, :, 50]]).all()
     assert gqa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_biased_decode_after_an_eviction_counts_rows(dtype):
+    """Weights from a plain call, eviction, then a decode with a bias, a window and a key range: all count the rows that
+    are left."""
+    import kv_cache_attention_gqa_b200 as gqa
+
+    B, h_q, h_kv, T, d, budget = 2, 8, 2, 400, 64, 96
+    q, k, v = (_randn((B, h, n, d), dtype, i) for i, h, n in ((1, h_q, 1), (2, h_kv, T), (3, h_kv, T)))
+    lens = [T, 250]
+    kd, vd, q1 = k.cuda(), v.cuda(), q[:, :, 0].cuda().contiguous()
+    _, lse = gqa.decode(q1, kd, vd, kv_len=lens, return_lse=True)
+    w = gqa.kv_weights(q1, kd, lse, kv_len=lens)
+    assert np.abs(w.double().sum(-1).cpu().numpy() - h_q / h_kv).max() < 1e-4
+    kept, new = gqa.kv_evict(kd, vd, w, budget, kv_len=lens, sink=2, recent=20)
+    assert new.tolist() == [budget, budget]
+    left = [torch.stack([torch.stack([x[b, g, kept[b, g].long().cpu()] for g in range(h_kv)]) for b in range(B)]) for x in (k, v)]
+    slopes, rg = torch.linspace(0.0, 0.3, h_q), torch.tensor([[10, 90], [0, 96]], dtype=torch.int32)
+    ref = oracle.modified_attention_ref(q.double(), *(x.double() for x in left), q_start=[budget - 1] * B, window=70,
+                                        slopes=slopes.numpy(), key_range=rg[:, None].numpy())
+    o, lse = gqa.decode(q1, kd, vd, kv_len=new, window=70, alibi_slopes=slopes.cuda(), key_range=rg.cuda(), return_lse=True)
+    _forward_close(o[:, :, None], lse[..., None], ref)
+    assert gqa.get_device_error() == 0
