@@ -10,7 +10,7 @@
 // loads. Calls whose 32-row tiles leave SMs without a block are bound by latency (two warps a scheduler waiting for
 // shared memory): they take tiles of 8 rows, and of 8 keys, with a warp to each. dq and dkdv need nothing of each
 // other and are blocks of one launch. Measured (B200), 2 x 6 heads of 67 rows over 2 KV heads, d = 96: forward 18 us,
-// backward 34 us (29, and 32 + 36 in two launches, with tiles of 32 rows and 16 keys); one warp per row with a shuffle
+// backward 32 us (29, and 32 + 36 in two launches, with tiles of 32 rows and 16 keys); one warp per row with a shuffle
 // reduction per key, the layout of the plain check-mode kernels, took 77 and 95 + 166 us.
 
 #include <cooperative_groups.h>
